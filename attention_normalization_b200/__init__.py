@@ -28,6 +28,9 @@ __all__ = ["qknorm_layerwise", "qknorm_headwise", "qknorm_qkv_gemm_stats", "qkno
            "qkv_workspace_bytes", "device_timeouts", "qknorm_tp_layerwise", "TpExchange", "TpPeerExchange",
            "qknorm_partial_stats", "qknorm_combine_apply", "qknorm_partial_stats_shards",
            "qknorm_combine_apply_shards", "gamma_dtype",
+           "qknorm_headwise_rope", "qknorm_headwise_rope_backward", "rope_backward_workspace_bytes",
+           "qknorm_rope_append", "qknorm_rope_append_kv4", "Kv4Cache", "kv4_cache", "qknorm_kv4_read",
+           "qknorm_kv4_attention", "kv4_attention_workspace_bytes",
            "qknorm_layerwise_plan", "qknorm_layerwise_host", "qknorm_packed_host",
            "plan_shape", "plan_grid", "regions_overlap", "qkv_gemm_schedule", "qkv_gemm_plan", "capi", "version", "QknLaunch", "QKNormError"]
 
@@ -607,3 +610,6 @@ def regions_overlap(a: tuple, b: tuple) -> bool:
 
 
 from .host_pipeline import qknorm_layerwise_host, qknorm_packed_host  # noqa: E402  (uses qknorm_layerwise)
+from .rope_cache import (Kv4Cache, kv4_attention_workspace_bytes, kv4_cache, qknorm_headwise_rope,  # noqa: E402
+                         qknorm_headwise_rope_backward, qknorm_kv4_attention, qknorm_kv4_read, qknorm_rope_append,
+                         qknorm_rope_append_kv4, rope_backward_workspace_bytes)

@@ -51,6 +51,7 @@ _dt = ctypes.c_int
 _st = ctypes.c_int
 _LAYERWISE_ARGS = [_vp, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i32, _i32, _f32, _dt]
 _HEADWISE_ARGS = [_vp, _vp, _vp, _i64, _i32, _vp, _vp, _vp, _i64, _i32, _i64, _i32, _f32, _dt]
+_APPEND_ARGS = [_vp, _vp, _vp, _i64, _i32, _vp, _vp, _i64, _vp, _i64, _i32, _i64, _i32, _vp, _i64, _i32, _i32, _vp]
 
 PROTOTYPES = {
     "qknorm_qkv_gemm_schedule": (_st, [_i64, _i32, _i32, _i32, _i32, _i32, _i64, ctypes.POINTER(QknGemmSchedule)]),
@@ -70,6 +71,18 @@ PROTOTYPES = {
     "qknorm_combine_apply_shards_launch": (_st, [_i32, _vp, _vp, _vp, _i64, _i32, _vp, _i32,
                                                  _vp, _vp, _vp, _i64, _i32, _vp, _i32, _i64, _f32, _dt, _vp,
                                                  ctypes.POINTER(QknLaunch)]),
+    "qknorm_headwise_rope": (_st, [_vp, _vp, _vp, _i64, _i32, _vp, _vp, _vp, _i64, _i32, _i64, _i32, _vp, _i64, _i32,
+                                   _i32, _vp, _f32, _dt, _vp]),
+    "qknorm_headwise_rope_backward": (_st, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32,
+                                            _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32,
+                                            _i64, _i32, _vp, _i64, _i32, _i32, _vp, _f32, _vp, _i64, _dt, _vp]),
+    "qknorm_headwise_rope_backward_workspace_bytes": (_i64, [_i64, _i32, _i32, _i32]),
+    "qknorm_rope_append": (_st, _APPEND_ARGS + [_vp, _vp, _vp, _vp, _i64, _i32, _vp, _f32, _dt, _vp]),
+    "qknorm_rope_append_kv4": (_st, _APPEND_ARGS + [_vp, _vp, _vp, _vp, _i64, _i32, _vp, _f32, _dt, _vp]),
+    "qknorm_kv4_read": (_st, [_vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _dt, _vp]),
+    "qknorm_kv4_attention": (_st, [_vp, _i64, _vp, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32,
+                                   _vp, _i32, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _f32, _vp, _i64, _dt, _vp]),
+    "qknorm_kv4_attention_workspace_bytes": (_i64, [_i64, _i32, _i32, _i32, _i32, _i32, _i32]),
     "qknorm_status_string": (ctypes.c_char_p, [_st]),
     "qknorm_qkv_gemm_stats": (_st, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i32, _i32, _i32, _i32,
                                     _vp, _vp, _dt, _vp]),

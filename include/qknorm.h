@@ -237,6 +237,172 @@ qkn_status qknorm_headwise(const void *q_in, void *q_out, const void *gamma_q, i
                            int64_t T, int32_t head_dim, float eps, qkn_dtype dtype, void *stream);
 
 /*
+ * Headwise QK-Norm and the rotary position embedding in one pass (what an
+ * attention layer does to its projected Q and K between the projection and the
+ * attention): each head is normalized as by qknorm_headwise,
+ *       n_j = (x_j * gamma_j) * r,
+ * kept in fp32, and rotated by its token's position before the one rounding:
+ *       a' = a * cos_i - b * sin_i,   b' = a * sin_i + b * cos_i
+ * for the pairs i < rotary_dim / 2, (a, b) = elements (i, i + rotary_dim / 2)
+ * of the head, or (2i, 2i + 1) with interleaved != 0.  Elements from
+ * rotary_dim on are normalized only.
+ *   q_in, q_out, gamma_q, q_stride, q_heads, k_...: as in qknorm_headwise
+ *         (out == in normalizes and rotates in place).
+ *   cos_sin : [table_rows][rotary_dim] fp32, contiguous: row p holds the
+ *         rotary_dim / 2 cosines of position p, then its sines.
+ *   positions : [T] int64, token t's row of the table.  A negative position
+ *         marks a padding token: its Q and K rows become zeros.  A position
+ *         >= table_rows gives rows of NaN; the table is never read past its end.
+ * ONE launch.  Rows move as 16-byte vectors when pointers, strides and cos_sin
+ * are 16-byte aligned, head_dim and rotary_dim are whole multiples of two
+ * vectors and head_dim is at most 64 vectors; otherwise an element-wise kernel
+ * runs.
+ * Errors: as qknorm_headwise, plus QKN_ERR_INVALID_ARG for an odd rotary_dim
+ * or one outside [0, head_dim], null or unaligned positions or cos_sin, an
+ * output overlapping them, or T * heads >= 2^31; QKN_ERR_UNSUPPORTED for
+ * head_dim > 1024.  (No paper counterpart: the page stops at the norm.)
+ */
+qkn_status qknorm_headwise_rope(const void *q_in, void *q_out, const void *gamma_q, int64_t q_stride, int32_t q_heads,
+                                const void *k_in, void *k_out, const void *gamma_k, int64_t k_stride, int32_t k_heads,
+                                int64_t T, int32_t head_dim, const float *cos_sin, int64_t table_rows,
+                                int32_t rotary_dim, int32_t interleaved, const int64_t *positions, float eps,
+                                qkn_dtype dtype, void *stream);
+
+/*
+ * Gradient of qknorm_headwise_rope.  With u = R(position)^T dy (the transposed
+ * rotation) and M = sum_j u_j gamma_j x_j over the head:
+ *       dx_j = r * (u_j * gamma_j - x_j * r^2 * M / head_dim),
+ *       dgamma_j = sum over tokens and heads of u_j * x_j * r.
+ *   q_in : the rows the forward call READ (not its outputs); dq_out : the
+ *         gradient of its outputs; dq_in : written; each with a row stride of
+ *         its own.  dq_in may be exactly dq_out or q_in (same base and stride).
+ *   dgamma_q, dgamma_k : [head_dim] fp32, overwritten (zeros when T == 0).
+ *   workspace : qknorm_headwise_rope_backward_workspace_bytes bytes, 4-byte
+ *         aligned: the CTAs' partial sums of dgamma, added in a fixed order
+ *         (results are the same run to run).
+ * Padding tokens (negative positions) get zero gradients and add nothing to
+ * dgamma; a position past the table makes its rows and dgamma NaN.  Two
+ * launches on `stream`.
+ * Errors: as qknorm_headwise_rope, plus QKN_ERR_UNSUPPORTED for E4M3 and
+ * QKN_ERR_INVALID_ARG for a null dgamma or a workspace that is too small.
+ */
+qkn_status qknorm_headwise_rope_backward(const void *q_in, int64_t q_stride, const void *dq_out, int64_t dq_out_stride,
+                                         void *dq_in, int64_t dq_in_stride, const void *gamma_q, float *dgamma_q,
+                                         int32_t q_heads, const void *k_in, int64_t k_stride, const void *dk_out,
+                                         int64_t dk_out_stride, void *dk_in, int64_t dk_in_stride, const void *gamma_k,
+                                         float *dgamma_k, int32_t k_heads, int64_t T, int32_t head_dim,
+                                         const float *cos_sin, int64_t table_rows, int32_t rotary_dim,
+                                         int32_t interleaved, const int64_t *positions, float eps, void *workspace,
+                                         int64_t workspace_bytes, qkn_dtype dtype, void *stream);
+/* Bytes of its workspace; -1 for sizes the call refuses. */
+int64_t qknorm_headwise_rope_backward_workspace_bytes(int64_t T, int32_t q_heads, int32_t k_heads, int32_t head_dim);
+
+/*
+ * Appends T tokens' keys and values to a paged cache, with the headwise norm
+ * and the position rotation applied on the way; the Q rows are normalized and
+ * rotated in the same launch.
+ *   q_in, q_out (stride q_stride, q_heads heads), k_in, v_in (kv_heads heads
+ *         each, strides k_stride and v_stride): rows of the projection, packed
+ *         or separate.  q_heads == 0: no Q rows (the q pointers are ignored).
+ *   gamma_q, gamma_k : [head_dim]; both null: rotation only, for rows that
+ *         qknorm_layerwise or qknorm_qkv_projection has normalized already.
+ *   cos_sin, positions, rotary_dim, interleaved, eps: as qknorm_headwise_rope.
+ *         V is stored as it is.
+ *   k_cache, v_cache : elements of `dtype`; the cell of token slot s, head h is
+ *         at base + (s / page_size) * strides[0] + (s % page_size) * strides[1]
+ *         + h * strides[2], strides in elements, head_dim elements contiguous
+ *         (pages of tokens of heads, pages of heads of tokens, or K and V
+ *         interleaved by page).  k_cache_strides and v_cache_strides are HOST
+ *         arrays of three.  Offsets are 64-bit.
+ *   slots : [T] int64, the cell each token goes to.  A slot that is negative or
+ *         >= num_pages * page_size is not written (padding rows); its Q row
+ *         still is.  Two tokens with the same slot leave that cell unspecified.
+ * ONE launch; cells no slot names are left as they were.
+ * Errors: as qknorm_headwise_rope, plus QKN_ERR_INVALID_ARG for only one of
+ * the gammas, cells that overlap one another, a cache overlapping any operand
+ * or the other cache, or bad page sizes.
+ */
+qkn_status qknorm_rope_append(const void *q_in, void *q_out, const void *gamma_q, int64_t q_stride, int32_t q_heads,
+                              const void *k_in, const void *gamma_k, int64_t k_stride, const void *v_in,
+                              int64_t v_stride, int32_t kv_heads, int64_t T, int32_t head_dim, const float *cos_sin,
+                              int64_t table_rows, int32_t rotary_dim, int32_t interleaved, const int64_t *positions,
+                              void *k_cache, const int64_t *k_cache_strides, void *v_cache,
+                              const int64_t *v_cache_strides, int64_t num_pages, int32_t page_size,
+                              const int64_t *slots, float eps, qkn_dtype dtype, void *stream);
+
+/*
+ * The 4-bit cache: four contiguous tensors, 16-byte aligned,
+ *   k_codes, v_codes   [num_pages][kv_heads][page_size][head_dim / 2] bytes,
+ *   k_scales, v_scales [num_pages][kv_heads][page_size][head_dim / 64] fp16.
+ * A head's vector y is held in groups of 64 elements: the scale is
+ * s = fp16(max |y| / 7) (saturated at 65504) and element j the code
+ * c_j = clamp(rint(y_j / s), -7, 7) (0 where s is 0), stored as c_j + 8 in a
+ * nibble: element 2i in the low half of byte i, 2i + 1 in the high half.  It
+ * stands for c_j * s.  Codes and scales are the correctly rounded ones of the
+ * formula in 64 bits, so they do not depend on the kernel variant.  A group
+ * with a NaN or an infinity gets a NaN scale and reads as NaN.
+ * head_dim is 64, 128 or 256 and page_size a multiple of 16 (else
+ * QKN_ERR_UNSUPPORTED).
+ *
+ * qknorm_rope_append_kv4 is qknorm_rope_append into it (float32, bfloat16 or
+ * float16 rows).  qknorm_kv4_read gives n cached tokens back as K and V rows
+ * [n rows, kv_heads * head_dim], each value rounded once; a slot outside the
+ * cache gives zeros.
+ */
+qkn_status qknorm_rope_append_kv4(const void *q_in, void *q_out, const void *gamma_q, int64_t q_stride, int32_t q_heads,
+                                  const void *k_in, const void *gamma_k, int64_t k_stride, const void *v_in,
+                                  int64_t v_stride, int32_t kv_heads, int64_t T, int32_t head_dim,
+                                  const float *cos_sin, int64_t table_rows, int32_t rotary_dim, int32_t interleaved,
+                                  const int64_t *positions, void *k_codes, void *k_scales, void *v_codes,
+                                  void *v_scales, int64_t num_pages, int32_t page_size, const int64_t *slots, float eps,
+                                  qkn_dtype dtype, void *stream);
+qkn_status qknorm_kv4_read(const void *k_codes, const void *k_scales, const void *v_codes, const void *v_scales,
+                           int64_t num_pages, int32_t page_size, int32_t kv_heads, int32_t head_dim,
+                           const int64_t *slots, int64_t n, void *k_out, int64_t k_stride, void *v_out,
+                           int64_t v_stride, qkn_dtype dtype, void *stream);
+
+/*
+ * Attention of query rows over the 4-bit paged cache, for decoding (one token
+ * per sequence) and for chunks of prompts, causal, with grouped heads:
+ * query head h reads KV head h / (q_heads / kv_heads).
+ *   q   : [T rows, stride q_stride], q_heads * head_dim wide, bfloat16 or
+ *         float16 (else QKN_ERR_UNSUPPORTED); out likewise (own stride).
+ *   lse : [T][q_heads] fp32 or null: log of the softmax sum (natural log).
+ *   block_table : [B][max_pages] int32, page numbers of each sequence.  Tokens
+ *         on a page outside [0, num_pages) count as absent.
+ *   seq_lens : [B] int32, cached tokens of each sequence, the rows' own tokens
+ *         among them (clipped to max_seq_len and to max_pages * page_size).
+ *   q_start : [B + 1] int32: sequence b's rows are q_start[b] .. q_start[b+1]-1,
+ *         at most max_q_len of them, the sequence's last tokens; null: row b is
+ *         sequence b's one query.  Rows of no sequence are left as they were.
+ *   Row i of n of a sequence of len tokens is at position p = len - n + i and
+ *         sees tokens t <= p, with window > 0 only t > p - window.
+ *   A row that sees no token gives zeros and lse = -infinity.
+ *   scale : multiplies q . k (1 / sqrt(head_dim) as a rule).
+ *   max_seq_len, max_q_len : bounds the host knows; they size the launch and
+ *         the workspace.
+ *   workspace : qknorm_kv4_attention_workspace_bytes bytes, 16-byte aligned:
+ *         partial results of a long cache split over the SMs.  Calls that may
+ *         run at the same time need workspaces of their own.
+ * Sums and softmax statistics are fp32.  At most two launches on `stream`.
+ * Errors: QKN_ERR_INVALID_ARG for bad sizes, strides, null or unaligned
+ * pointers, q_heads not a multiple of kv_heads, an output overlapping another
+ * operand, T * q_heads >= 2^31 or a small workspace; QKN_ERR_UNSUPPORTED as
+ * above and for more than 65535 sequences or 65535 * 64 query rows per
+ * sequence and KV head.
+ */
+qkn_status qknorm_kv4_attention(const void *q, int64_t q_stride, void *out, int64_t out_stride, float *lse,
+                                int32_t q_heads, const void *k_codes, const void *k_scales, const void *v_codes,
+                                const void *v_scales, int64_t num_pages, int32_t page_size, int32_t kv_heads,
+                                int32_t head_dim, const int32_t *block_table, int32_t max_pages,
+                                const int32_t *seq_lens, const int32_t *q_start, int64_t T, int32_t B,
+                                int32_t max_q_len, int32_t max_seq_len, int32_t window, float scale, void *workspace,
+                                int64_t workspace_bytes, qkn_dtype dtype, void *stream);
+/* Bytes of its workspace (0 when the cache is not split); -1 for bad sizes. */
+int64_t qknorm_kv4_attention_workspace_bytes(int64_t T, int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                             int32_t max_q_len, int32_t max_seq_len);
+
+/*
  * QKV projection with Phase A's partial sums in the GEMM epilogue (Background:
  * in a Pre-LN layer linear projections of the hidden state produce Q, K and V,
  * and QK-Norm sits between the Q/K projections and attention; Phase A: the
