@@ -32,6 +32,10 @@ struct Kv4AttnParams {
     int64_t T, table_stride, num_pages;
     int32_t max_pages, page_size, B, q_heads, kv_heads, group, max_q_len, max_seq_len, window;
     float scale;
+    int32_t q_vector, out_vector;  // rows move as 16-byte (8-byte) vectors
+    int32_t n_tiles;               // query tile: 8 * n_tiles rows
+    int32_t chunk_tiles, splits;   // 16-token tiles of a chunk, chunks at most
+    float *part_o, *part_s;        // [T][q_heads][splits][head_dim] and (exponent, sum) pairs
 };
 
 // Rows and cached tokens of sequence b, kept inside the buffers.
@@ -55,64 +59,558 @@ __device__ __forceinline__ Seq sequence(const Kv4AttnParams &p, int b) {
     return s;
 }
 
-// One warp per row and query head; lane l holds elements l * D / 32 ...
-template <typename E, int D>
-__global__ void __launch_bounds__(256) kv4_attention_simple(const __grid_constant__ Kv4AttnParams p) {
-    pdl_wait_and_release();
-    constexpr int N = D / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int b = blockIdx.y;
-    const Seq s = sequence(p, b);
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + warp;
-    const int i = static_cast<int>(item / p.q_heads), h = static_cast<int>(item % p.q_heads);
-    if (i >= s.rows) return;
-    const int64_t row = s.row0 + i;
-    const int kvh = h / p.group;
-    float q[N], o[N];
-    const char *qp = p.q + row * p.q_stride + static_cast<int64_t>(h) * D * sizeof(E);
-    for (int e = 0; e < N; ++e) {
-        q[e] = Elem<E>::to_float(reinterpret_cast<const typename Elem<E>::Bits *>(qp)[lane * N + e]) * p.scale;
-        o[e] = 0.0f;
+// Four elements of the output, sum / total (zeros for a row without tokens).
+template <typename E>
+__device__ __forceinline__ void store_row(const Kv4AttnParams &p, int64_t row, int64_t at, const float4 &sum, float total) {
+    const float f = total == 0.0f ? 0.0f : 1.0f / total;
+    typename Elem<E>::Bits *out = reinterpret_cast<typename Elem<E>::Bits *>(p.out + row * p.out_stride) + at;
+    const uint32_t lo = Elem<E>::narrow_word(f2(sum.x * f, sum.y * f)), hi = Elem<E>::narrow_word(f2(sum.z * f, sum.w * f));
+    if (p.out_vector) {
+        *reinterpret_cast<uint2 *>(out) = make_uint2(lo, hi);
+    } else {
+        out[0] = static_cast<uint16_t>(lo);
+        out[1] = static_cast<uint16_t>(lo >> 16);
+        out[2] = static_cast<uint16_t>(hi);
+        out[3] = static_cast<uint16_t>(hi >> 16);
     }
-    float m = -INFINITY, l = 0.0f;
-    const int pos = s.len - s.rows + i;
-    const int first = p.window > 0 && pos - p.window + 1 > 0 ? pos - p.window + 1 : 0;
-    for (int t = first; t <= pos; ++t) {
-        const int32_t page = p.block_table[b * p.table_stride + t / p.page_size];
-        if (page < 0 || page >= p.num_pages) continue;
-        const int64_t cell = (static_cast<int64_t>(page) * p.kv_heads + kvh) * p.page_size + t % p.page_size;
-        const int at = lane * N;
-        float sc[2];
-        float v[2][N];
-        for (int kv = 0; kv < 2; ++kv) {
-            sc[kv] = __half2float(p.scales[kv][cell * (D / kKv4Group) + at / kKv4Group]);
-            for (int e = 0; e < N; ++e) {
-                const uint8_t c = p.codes[kv][cell * (D / 2) + (at + e) / 2];
-                v[kv][e] = static_cast<float>(static_cast<int>((e & 1) ? c >> 4 : c & 15) - 8) * sc[kv];
+}
+__device__ __forceinline__ float finish_lse(float m, float total) {  // base 2 -> natural
+    return total == 0.0f ? -INFINITY : (m + log2f(total)) * 0.6931471805599453f;
+}
+
+// ----------------------------------------------------------------------------
+// One CTA takes a tile of 8 * NT query rows (rows of one sequence that read the
+// same KV head: row r = token r / group, head r % group) and a chunk of the
+// sequence's tokens; its warps take the chunk's 16-token tiles in turn, each
+// with its own running maximum, sum and output, joined once at the end.
+//
+// Scores are formed transposed, S^T = K Q^T, and so is the output, O^T = V^T P^T,
+// with mma.m16n8k16: the 16 rows are cached tokens (or value dims), the 8
+// columns query rows, so that one decoded token with up to 8 heads per KV head
+// wastes nothing of a tile, and a thread's score columns are its output
+// columns.  The codes are the A operand straight from registers: a nibble
+// becomes a half by one logic operation (1024 + n or 64 + n) and one exact
+// subtraction.  The group scales stay out of the products: a key's scale
+// multiplies the finished dot product of its group, a value's scale its
+// weight, so each product is code * half, exact in fp32.
+//
+// Queries are scaled by a power of two per row to fit halves without loss
+// (elements 2^-24 below the row's largest lose bits that fp32 sums of the row
+// would not see either).  Weights are rounded to halves, 2^-11 relative; they
+// are kept between 2^-31 and 2^8 of the reference by normalising
+// p * (value scale), not p alone, and by an offset of 2^7.  The row sum l takes
+// the unrounded weights.
+//
+// The reference exponent moves only when a weight would exceed 2^8 times it
+// (one vote per tile); the exact maximum is not needed, as l and O share it.
+constexpr int kAttnWarps = 4;
+constexpr int kStages = 4;
+constexpr float kOffset = 7.0f, kGrow = 8.0f;
+
+template <int D>
+struct Kv4Tile {  // bytes of one 16-token tile of one KV head
+    static constexpr int kGroups = D / kKv4Group;
+    static constexpr int kCodes = 16 * D / 2;
+    static constexpr int kScales = 16 * kGroups * 2;
+    static constexpr int kBytes = 2 * (kCodes + kScales);  // K codes, V codes, K scales, V scales
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t nib(uint32_t w, uint32_t mask, uint32_t magic) {  // (w & mask) | magic
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(mask), "r"(magic));
+    return d;
+}
+__device__ __forceinline__ uint32_t sub_half2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// Nibbles i and i + 4 of w as halves (code), i = 0 .. 3.
+__device__ __forceinline__ void codes8(uint32_t w, uint32_t (&h)[4]) {
+    const uint32_t x = w >> 8;
+    h[0] = sub_half2(nib(w, 0x000F000Fu, 0x64006400u), 0x64086408u);  // 1024 + n - 1032
+    h[1] = sub_half2(nib(w, 0x00F000F0u, 0x54005400u), 0x54805480u);  // 64 + n - 72
+    h[2] = sub_half2(nib(x, 0x000F000Fu, 0x64006400u), 0x64086408u);
+    h[3] = sub_half2(nib(x, 0x00F000F0u, 0x54005400u), 0x54805480u);
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
+    return d;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Which tokens the rows [r0, r0 + n) of a sequence see: tiles [first, last) of 16.
+struct TileRange {
+    int first, last;
+};
+__device__ __forceinline__ TileRange tile_range(const Kv4AttnParams &p, const Seq &s, int r0, int n) {
+    const int rows = s.rows * p.group;
+    const int r1 = (r0 + n < rows ? r0 + n : rows) - 1;
+    const int lo = s.len - s.rows + r0 / p.group, hi = s.len - s.rows + r1 / p.group;  // positions
+    TileRange t{0, hi < 0 ? 0 : hi / 16 + 1};
+    if (p.window > 0 && lo - p.window + 1 > 0) t.first = (lo - p.window + 1) / 16;
+    if (t.first > t.last) t.first = t.last;
+    return t;
+}
+
+template <typename E, int D, int NT>
+__global__ void __launch_bounds__(kAttnWarps * 32) kv4_attention_kernel(const __grid_constant__ Kv4AttnParams p) {
+    using Tile = Kv4Tile<D>;
+    constexpr int G = Tile::kGroups, R = 8 * NT;
+    extern __shared__ __align__(128) char smem[];
+    pdl_wait_and_release();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    const int b = blockIdx.z, kvh = blockIdx.y % p.kv_heads, r0 = static_cast<int>(blockIdx.y / p.kv_heads) * R;
+    const Seq seq = sequence(p, b);
+    const int rows = seq.rows * p.group;
+    if (r0 >= rows) return;
+    const TileRange range = tile_range(p, seq, r0, R);
+    const int chunk_first = range.first + static_cast<int>(blockIdx.x) * p.chunk_tiles;
+    if (blockIdx.x > 0 && chunk_first >= range.last) return;  // chunk 0 also answers for rows without tokens
+    const int chunk_last = min(chunk_first + p.chunk_tiles, range.last);
+    const int base_pos = seq.len - seq.rows;  // position of the sequence's row 0
+
+    char *mine = smem + warp * (kStages * Tile::kBytes);
+    const uint32_t mine_u32 = smem_u32(mine);
+    const int32_t *table = p.block_table + b * p.table_stride;
+    uint32_t held = 0;  // bit s: stage s holds a tile that is there
+
+    auto page_of = [&](int tile) -> int32_t {
+        if (tile >= chunk_last) return -1;
+        return __ldg(table + static_cast<uint32_t>(tile * 16) / static_cast<uint32_t>(p.page_size));
+    };
+    auto issue = [&](int tile, int32_t page, int stage) {
+        held &= ~(1u << stage);
+        if (page >= 0 && page < p.num_pages) {
+            held |= 1u << stage;
+            const int off = static_cast<uint32_t>(tile * 16) % static_cast<uint32_t>(p.page_size);
+            const int64_t cell = (static_cast<int64_t>(page) * p.kv_heads + kvh) * p.page_size + off;
+            const uint32_t dst = mine_u32 + stage * Tile::kBytes;
+            const uint8_t *k = p.codes[0] + cell * (D / 2), *v = p.codes[1] + cell * (D / 2);
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {  // 16-byte pieces: [group][token][half], V's tokens 0, 2, .. 14, 1, 3, ..
+                const int piece = i * 32 + lane, token = piece / (D / 32), part = piece % (D / 32);
+                const uint32_t at = (part / 2) * 512 + (part & 1) * 16;
+                cp_async16(dst + at + token * 32, k + piece * 16);
+                cp_async16(dst + Tile::kCodes + at + (((token & 1) << 3) | (token >> 1)) * 32, v + piece * 16);
+            }
+            if (lane < 2 * (Tile::kScales / 16)) {
+                const int kv = lane >= Tile::kScales / 16, piece = lane - kv * (Tile::kScales / 16);
+                cp_async16(dst + 2 * Tile::kCodes + kv * Tile::kScales + piece * 16,
+                           reinterpret_cast<const char *>(p.scales[kv] + cell * G) + piece * 16);
             }
         }
-        float dot = 0.0f;
-        for (int e = 0; e < N; ++e) dot += q[e] * v[0][e];
-        dot = warp_sum(dot);
-        const float mn = fmaxf(m, dot);
-        const float up = mn == -INFINITY ? 1.0f : __expf(m - mn), w = dot == -INFINITY ? 0.0f : __expf(dot - mn);
-        l = l * up + w;
-        for (int e = 0; e < N; ++e) o[e] = o[e] * up + w * v[1][e];
-        m = mn;
+        cp_commit();
+    };
+
+    int tile = chunk_first + warp;
+    int32_t page = page_of(tile);
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+        const int32_t next = page_of(tile + (s + 1) * kAttnWarps);
+        issue(tile + s * kAttnWarps, page, s);
+        page = next;
     }
-    char *op = p.out + row * p.out_stride + static_cast<int64_t>(h) * D * sizeof(E);
+
+    // Queries: this thread's B operands (row 8 j + g, dims 64 gr + 16 c .. + 15)
+    // and, for its score columns 2c and 2c + 1, the row's factor and limits.
+    uint32_t q[NT][G][8];
+    float qmul[NT][2];
+    int top[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int r = r0 + 8 * j + g;
+        float x[G][16];
+        float amax = 0.0f;
+        const int64_t row = seq.row0 + r / p.group;
+        const int head = kvh * p.group + r % p.group;
+        const char *src = p.q + row * p.q_stride + (static_cast<int64_t>(head) * D + 16 * c) * sizeof(E);
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) {
+            if (p.q_vector) {
+                uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                if (r < rows) {
+                    v[0] = *reinterpret_cast<const uint4 *>(src + gr * 128);
+                    v[1] = *reinterpret_cast<const uint4 *>(src + gr * 128 + 16);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    F2 w[4];
+                    Elem<E>::widen(v[h], w);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[gr][8 * h + 2 * e] = f2_lo(w[e]);
+                        x[gr][8 * h + 2 * e + 1] = f2_hi(w[e]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    x[gr][e] = r < rows ? Elem<E>::to_float(
+                                              reinterpret_cast<const typename Elem<E>::Bits *>(src + gr * 128)[e])
+                                        : 0.0f;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[gr][e]));
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+        int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+        ex = amax == 0.0f ? 10 : max(ex, -100);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + 10 - ex) << 23);  // 2^(10 - ex)
+        // back, times the caller's scale and log2(e)
+        const float mul = p.scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 - 10 + ex) << 23);
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+            for (int w = 0; w < 2; ++w)  // word w of the codes: pairs (i, i + 4)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    q[j][gr][4 * w + i] = pack_half2(x[gr][8 * w + i] * up, x[gr][8 * w + i + 4] * up);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            qmul[j][e] = __shfl_sync(0xFFFFFFFFu, mul, (2 * c + e) * 4);
+            top[j][e] = base_pos + (r0 + 8 * j + 2 * c + e) / p.group;
+        }
+    }
+    const int lowest = base_pos + r0 / p.group;                                    // the tile's first row
+    const int highest = base_pos + (min(r0 + R, rows) - 1) / p.group;
+
+    float o[NT][D / 16][4] = {};
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) m[j][0] = m[j][1] = -INFINITY, l[j][0] = l[j][1] = 0.0f;
+
+    int stage = 0;
+    for (; tile < chunk_last; tile += kAttnWarps) {
+        {
+            const int ahead = tile + (kStages - 1) * kAttnWarps;
+            const int32_t next = page_of(ahead + kAttnWarps);
+            issue(ahead, page, (stage + kStages - 1) % kStages);
+            page = next;
+        }
+        cp_wait<kStages - 1>();
+        __syncwarp();
+        if (held & (1u << stage)) {
+            const char *kc = mine + stage * Tile::kBytes, *vc = kc + Tile::kCodes;
+            const __half *ks = reinterpret_cast<const __half *>(kc + 2 * Tile::kCodes);
+            const __half *vs = ks + 16 * G;
+            float s[NT][4];
+            float vscale[G][2];
+            float lv[2];
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+                const uint2 ka = *reinterpret_cast<const uint2 *>(kc + gr * 512 + g * 32 + c * 8);
+                const uint2 kb = *reinterpret_cast<const uint2 *>(kc + gr * 512 + (g + 8) * 32 + c * 8);
+                const float sa = __half2float(ks[g * G + gr]), sb = __half2float(ks[(g + 8) * G + gr]);
+                vscale[gr][0] = __half2float(vs[g * G + gr]);
+                vscale[gr][1] = __half2float(vs[(g + 8) * G + gr]);
+                uint32_t a[2][4], bq[2][4];
+                codes8(ka.x, a[0]);
+                codes8(ka.y, a[1]);
+                codes8(kb.x, bq[0]);
+                codes8(kb.y, bq[1]);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int w = 0; w < 2; ++w)
+#pragma unroll
+                        for (int i = 0; i < 4; i += 2)
+                            mma16816(acc, a[w][i], bq[w][i], a[w][i + 1], bq[w][i + 1], q[j][gr][4 * w + i],
+                                     q[j][gr][4 * w + i + 1]);
+                    if (gr == 0) {
+                        s[j][0] = acc[0] * sa;
+                        s[j][1] = acc[1] * sa;
+                        s[j][2] = acc[2] * sb;
+                        s[j][3] = acc[3] * sb;
+                    } else {
+                        s[j][0] = fmaf(acc[0], sa, s[j][0]);
+                        s[j][1] = fmaf(acc[1], sa, s[j][1]);
+                        s[j][2] = fmaf(acc[2], sb, s[j][2]);
+                        s[j][3] = fmaf(acc[3], sb, s[j][3]);
+                    }
+                }
+            }
+            // log2 of each token's largest value scale, kept to what halves can hold
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                float v = vscale[0][t];
+#pragma unroll
+                for (int gr = 1; gr < G; ++gr) v = fmaxf(v, vscale[gr][t]);
+                lv[t] = fminf(fmaxf(lg2(v), -24.0f), 16.0f);
+            }
+            const int t0 = tile * 16;
+            const bool masked = t0 + 15 > lowest || (p.window > 0 && t0 <= highest - p.window);
+            bool grow = false;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[j][e] *= qmul[j][e & 1];
+                    if (masked) {
+                        const int t = t0 + g + (e & 2) * 4;
+                        const int pos = top[j][e & 1];
+                        if (t > pos || (p.window > 0 && t <= pos - p.window)) s[j][e] = -INFINITY;
+                    }
+                    grow |= s[j][e] + lv[e >> 1] > m[j][e & 1] + kGrow;
+                }
+            if (__any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = fmaxf(s[j][e] + lv[0], s[j][e + 2] + lv[1]);
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+                        const float mn = fmaxf(m[j][e], x);
+                        const float f = mn == m[j][e] ? 1.0f : ex2(m[j][e] - mn);
+                        m[j][e] = mn;
+                        l[j][e] *= f;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            o[j][i][e] *= f;
+                            o[j][i][e + 2] *= f;
+                        }
+                    }
+            }
+            uint32_t pb[NT][G][2];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float ref = m[j][e & 1] == -INFINITY ? 0.0f : m[j][e & 1];
+                    w[e] = ex2(s[j][e] - ref + kOffset);
+                }
+                l[j][0] += w[0] + w[2];
+                l[j][1] += w[1] + w[3];
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr) {
+                    float x[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] = w[e] * vscale[gr][e >> 1];
+                    if (masked) {  // a masked token's scale may be anything
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (w[e] == 0.0f) x[e] = 0.0f;
+                    }
+                    pb[j][gr][0] = transpose8x8(pack_half2(x[0], x[1]));
+                    pb[j][gr][1] = transpose8x8(pack_half2(x[2], x[3]));
+                }
+            }
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+                const char *vg = vc + gr * 512 + g * 4;
+                const uint32_t w0 = *reinterpret_cast<const uint32_t *>(vg + c * 32);          // token 2c
+                const uint32_t w1 = *reinterpret_cast<const uint32_t *>(vg + (8 + c) * 32);    // 2c + 1
+                const uint32_t w2 = *reinterpret_cast<const uint32_t *>(vg + (4 + c) * 32);    // 2c + 8
+                const uint32_t w3 = *reinterpret_cast<const uint32_t *>(vg + (12 + c) * 32);   // 2c + 9
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {  // dims 8g + 4h .. + 3: pairs of tokens
+                    const uint32_t sel = h ? 0x7632u : 0x5410u;
+                    uint32_t a[4], bq[4];
+                    codes8(__byte_perm(w0, w1, sel), a);
+                    codes8(__byte_perm(w2, w3, sel), bq);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+                            mma16816(o[j][gr * 4 + h * 2 + i], a[2 * i], a[2 * i + 1], bq[2 * i], bq[2 * i + 1],
+                                     pb[j][gr][0], pb[j][gr][1]);
+                }
+            }
+        }
+        __syncwarp();
+        stage = (stage + 1) % kStages;
+    }
+    cp_wait<0>();
+    __syncwarp();
+
+    // Join the warps: O, the exponent m - kOffset and l of each row, in shared memory.
+    float *part = reinterpret_cast<float *>(mine);
+    float *stat = part + R * D;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            l[j][e] += __shfl_xor_sync(0xFFFFFFFFu, l[j][e], 4);
+            l[j][e] += __shfl_xor_sync(0xFFFFFFFFu, l[j][e], 8);
+            l[j][e] += __shfl_xor_sync(0xFFFFFFFFu, l[j][e], 16);
+            const int r = 8 * j + 2 * c + e;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)  // dims 64 gr + 8 g + 2 (i % 4), + 1
+                *reinterpret_cast<float2 *>(part + r * D + (i / 4) * 64 + g * 8 + (i % 4) * 2) =
+                    make_float2(o[j][i][e], o[j][i][e + 2]);
+            if (g == 0) {
+                stat[r] = m[j][e] == -INFINITY ? (l[j][e] == 0.0f ? -INFINITY : -kOffset) : m[j][e] - kOffset;
+                stat[R + r] = l[j][e];
+            }
+        }
+    __syncthreads();
+    constexpr int kStride = kStages * Tile::kBytes / 4;
+    const float *all = reinterpret_cast<const float *>(smem);
+    for (int i = threadIdx.x; i < R * (D / 4); i += kAttnWarps * 32) {
+        const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+        if (r0 + r >= rows) break;
+        float top_m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) top_m = fmaxf(top_m, all[w * kStride + R * D + r]);
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float total = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) {
+            const float *pw = all + w * kStride;
+            const float mw = pw[R * D + r];
+            const float f = mw == -INFINITY ? 0.0f : ex2(mw - top_m);
+            const float4 v = *reinterpret_cast<const float4 *>(pw + r * D + d);
+            sum.x = fmaf(v.x, f, sum.x);
+            sum.y = fmaf(v.y, f, sum.y);
+            sum.z = fmaf(v.z, f, sum.z);
+            sum.w = fmaf(v.w, f, sum.w);
+            total = fmaf(pw[R * D + R + r], f, total);
+        }
+        const int64_t row = seq.row0 + (r0 + r) / p.group;
+        const int head = kvh * p.group + (r0 + r) % p.group;
+        if (p.splits > 1) {
+            const int64_t cell = (row * p.q_heads + head) * p.splits + blockIdx.x;
+            *reinterpret_cast<float4 *>(p.part_o + cell * D + d) = sum;
+            if (d == 0) reinterpret_cast<float2 *>(p.part_s)[cell] = make_float2(top_m, total);
+        } else {
+            store_row<E>(p, row, head * D + d, sum, total);
+            if (d == 0 && p.lse) p.lse[row * p.q_heads + head] = finish_lse(top_m, total);
+        }
+    }
+}
+
+// Joins the chunks of each row: one warp per row and query head.
+template <typename E, int D>
+__global__ void __launch_bounds__(128) kv4_join_kernel(const __grid_constant__ Kv4AttnParams p) {
+    pdl_wait_and_release();
+    const int lane = threadIdx.x & 31;
+    const Seq seq = sequence(p, blockIdx.y);
+    const int item = static_cast<int>(blockIdx.x) * 4 + static_cast<int>(threadIdx.x >> 5);
+    const int i = item / p.q_heads, head = item % p.q_heads;
+    if (i >= seq.rows) return;
+    const int64_t row = seq.row0 + i;
+    const int tile_rows = 8 * p.n_tiles;
+    const int r = i * p.group + head % p.group;
+    const TileRange range = tile_range(p, seq, r / tile_rows * tile_rows, tile_rows);
+    const int n = max(1, (range.last - range.first + p.chunk_tiles - 1) / p.chunk_tiles);
+    const int64_t cell = (row * p.q_heads + head) * p.splits;
+    const float2 *stat = reinterpret_cast<const float2 *>(p.part_s) + cell;
+    float top_m = -INFINITY;
+    for (int k = lane; k < n; k += 32) top_m = fmaxf(top_m, stat[k].x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top_m = fmaxf(top_m, __shfl_xor_sync(0xFFFFFFFFu, top_m, off));
+    constexpr int N = D / 128 > 0 ? D / 128 : 1;
+    float4 sum[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) sum[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float total = 0.0f;
+    const int d0 = lane * 4;
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+        const float2 st = stat[k];
+        const float f = st.x == -INFINITY ? 0.0f : ex2(st.x - top_m);
+        total = fmaf(st.y, f, total);
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (d0 + e * 128 < D) {
+                const float4 v = *reinterpret_cast<const float4 *>(p.part_o + (cell + k) * D + d0 + e * 128);
+                sum[e].x = fmaf(v.x, f, sum[e].x);
+                sum[e].y = fmaf(v.y, f, sum[e].y);
+                sum[e].z = fmaf(v.z, f, sum[e].z);
+                sum[e].w = fmaf(v.w, f, sum[e].w);
+            }
+    }
+#pragma unroll
     for (int e = 0; e < N; ++e)
-        reinterpret_cast<typename Elem<E>::Bits *>(op)[lane * N + e] = Elem<E>::from_float(l == 0.0f ? 0.0f : o[e] / l);
-    if (lane == 0 && p.lse) p.lse[row * p.q_heads + h] = l == 0.0f ? -INFINITY : m + __logf(l);
+        if (d0 + e * 128 < D) store_row<E>(p, row, head * D + d0 + e * 128, sum[e], total);
+    if (lane == 0 && p.lse) p.lse[row * p.q_heads + head] = finish_lse(top_m, total);
 }
 
 using namespace checks;
 
+// How a call is cut up, from sizes the host knows.
+struct Plan {
+    int32_t n_tiles, row_tiles, chunk_tiles, splits;
+};
+constexpr int64_t kSlots = 148 * 4;  // resident CTAs on a B200
+
+Plan plan(int32_t B, int32_t q_heads, int32_t kv_heads, int32_t max_q_len, int32_t max_seq_len) {
+    Plan pl{};
+    const int64_t rows = (int64_t)max_q_len * (q_heads / kv_heads);
+    pl.n_tiles = rows <= 8 ? 1 : 2;
+    const int64_t tiles = (rows + 8 * pl.n_tiles - 1) / (8 * pl.n_tiles);
+    pl.row_tiles = tiles > INT32_MAX ? INT32_MAX : (int32_t)tiles;
+    const int64_t units = (int64_t)(B < 1 ? 1 : B) * kv_heads * tiles;
+    const int64_t len_tiles = ((int64_t)max_seq_len + 15) / 16;
+    // chunks of at least 256 tokens, as many as give every SM several
+    int64_t want = (4 * kSlots + units - 1) / units;
+    int64_t chunk = (len_tiles + want - 1) / want;
+    if (chunk < 16) chunk = 16;
+    pl.chunk_tiles = (int32_t)chunk;
+    pl.splits = (int32_t)((len_tiles + chunk - 1) / chunk);
+    if (pl.splits < 1) pl.splits = 1;
+    return pl;
+}
+
+template <typename E, int D, int NT>
+qkn_status launch_attention(const Kv4AttnParams &p, dim3 grid, dim3 join_grid, void *stream) {
+    constexpr size_t smem = (size_t)kAttnWarps * kStages * Kv4Tile<D>::kBytes;
+    static_assert((size_t)8 * NT * (D + 2) * 4 <= kStages * Kv4Tile<D>::kBytes, "a warp's partial result must fit its ring");
+    const void *fn = (const void *)kv4_attention_kernel<E, D, NT>;
+    if (smem > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return launched(e);
+    }
+    qkn_status st = launched(launch_pdl(fn, grid, kAttnWarps * 32, smem, stream, p));
+    if (st != QKN_OK || p.splits == 1) return st;
+    return launched(launch_pdl((const void *)kv4_join_kernel<E, D>, join_grid, 128, 0, stream, p));
+}
 template <typename E>
-const void *simple_kernel(int d) {
-    return d == 64    ? (const void *)kv4_attention_simple<E, 64>
-           : d == 128 ? (const void *)kv4_attention_simple<E, 128>
-                      : (const void *)kv4_attention_simple<E, 256>;
+qkn_status launch_attention(const Kv4AttnParams &p, int d, dim3 grid, dim3 join_grid, void *stream) {
+    if (p.n_tiles == 1)
+        return d == 64    ? launch_attention<E, 64, 1>(p, grid, join_grid, stream)
+               : d == 128 ? launch_attention<E, 128, 1>(p, grid, join_grid, stream)
+                          : launch_attention<E, 256, 1>(p, grid, join_grid, stream);
+    return d == 64    ? launch_attention<E, 64, 2>(p, grid, join_grid, stream)
+           : d == 128 ? launch_attention<E, 128, 2>(p, grid, join_grid, stream)
+                      : launch_attention<E, 256, 2>(p, grid, join_grid, stream);
 }
 
 }  // namespace
@@ -125,8 +623,11 @@ extern "C" {
 
 int64_t qknorm_kv4_attention_workspace_bytes(int64_t T, int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                              int32_t max_q_len, int32_t max_seq_len) {
-    if (T < 0 || B < 0 || q_heads < 1 || kv_heads < 1 || head_dim < 1 || max_q_len < 1 || max_seq_len < 0) return -1;
-    return 0;
+    if (T < 0 || B < 0 || q_heads < 1 || kv_heads < 1 || head_dim < 1 || max_q_len < 1 || max_seq_len < 0 ||
+        q_heads % kv_heads != 0 || head_dim > kRopeMaxHeadDim || T >= ((int64_t)1 << 31) / q_heads)
+        return -1;
+    const Plan pl = plan(B, q_heads, kv_heads, max_q_len, max_seq_len);
+    return pl.splits == 1 ? 0 : T * q_heads * pl.splits * (head_dim + 2) * 4;
 }
 
 qkn_status qknorm_kv4_attention(const void *q, int64_t q_stride, void *out, int64_t out_stride, float *lse,
@@ -167,6 +668,9 @@ qkn_status qknorm_kv4_attention(const void *q, int64_t q_stride, void *out, int6
         return fail(QKN_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)need);
     if (need > 0 && !aligned16(workspace)) return fail(QKN_ERR_INVALID_ARG, "the workspace must be 16-byte aligned");
     if (T == 0 || B == 0) return ok();
+    const Plan pl = plan(B, q_heads, kv_heads, max_q_len, max_seq_len);
+    if ((int64_t)max_q_len * q_heads > (1 << 20) || (int64_t)pl.row_tiles * kv_heads > 65535)
+        return fail(QKN_ERR_UNSUPPORTED, "max_q_len = %d too long: call in chunks", max_q_len);
     Span w[3], r[8];
     int nw = 0, nr = 0;
     w[nw++] = Span{out, width * 2, out_stride * 2, T, "out"};
@@ -209,9 +713,17 @@ qkn_status qknorm_kv4_attention(const void *q, int64_t q_stride, void *out, int6
     p.max_seq_len = max_seq_len;
     p.window = window;
     p.scale = scale;
-    const void *fn = dtype == QKN_BF16 ? simple_kernel<__nv_bfloat16>(head_dim) : simple_kernel<__half>(head_dim);
-    const int64_t items = (int64_t)max_q_len * q_heads;
-    return launched(launch_pdl(fn, dim3((unsigned)((items + 7) / 8), (unsigned)B), 256, 0, stream, p));
+    p.q_vector = aligned16(q) && p.q_stride % 16 == 0;
+    p.out_vector = ((uintptr_t)out & 7u) == 0 && p.out_stride % 8 == 0;
+    p.n_tiles = pl.n_tiles;
+    p.chunk_tiles = pl.chunk_tiles;
+    p.splits = pl.splits;
+    p.part_o = static_cast<float *>(workspace);
+    p.part_s = p.part_o + T * q_heads * pl.splits * head_dim;
+    const dim3 grid((unsigned)pl.splits, (unsigned)(pl.row_tiles * kv_heads), (unsigned)B);
+    const dim3 join_grid((unsigned)(((int64_t)max_q_len * q_heads + 3) / 4), (unsigned)B);
+    return dtype == QKN_BF16 ? launch_attention<__nv_bfloat16>(p, head_dim, grid, join_grid, stream)
+                             : launch_attention<__half>(p, head_dim, grid, join_grid, stream);
 }
 
 }  // extern "C"
