@@ -87,6 +87,8 @@ inline qkn_status check_kv4(int64_t num_pages, int32_t page_size, int32_t kv_hea
     if (page_size % kKv4PageMultiple != 0)
         return fail(QKN_ERR_UNSUPPORTED, "the 4-bit cache's page_size must be a multiple of %d, got %d", kKv4PageMultiple,
                     page_size);
+    if ((int64_t)kv_heads * page_size * (head_dim / 2) >= ((int64_t)1 << 31))
+        return fail(QKN_ERR_UNSUPPORTED, "a page of the 4-bit cache must stay below 2 GiB");
     const __int128 cells = (__int128)num_pages * kv_heads * page_size;
     if (cells * head_dim >= ((__int128)1 << 60)) return fail(QKN_ERR_INVALID_ARG, "cache extent overflows");
     *codes = (int64_t)cells * (head_dim / 2);

@@ -101,11 +101,11 @@ __device__ __forceinline__ float finish_lse(float m, float total) {  // base 2 -
 // p * (value scale), not p alone, and by an offset of 2^7.  The row sum l takes
 // the unrounded weights.
 //
-// The reference exponent moves only when a weight would exceed 2^8 times it
-// (one vote per tile); the exact maximum is not needed, as l and O share it.
+// The reference exponent moves only when a scaled weight would exceed 2^15 (one
+// vote per tile); the exact maximum is not needed, as l and O share it.
 constexpr int kAttnWarps = 4;
 constexpr int kStages = 4;
-constexpr float kOffset = 7.0f, kGrow = 8.0f;
+constexpr float kOffset = 7.0f, kLargest = 32768.0f;
 
 template <int D>
 struct Kv4Tile {  // bytes of one 16-token tile of one KV head
@@ -149,6 +149,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// d = A B (no addend).
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t d;
@@ -203,46 +210,58 @@ __global__ void __launch_bounds__(kAttnWarps * 32) kv4_attention_kernel(const __
     const int base_pos = seq.len - seq.rows;  // position of the sequence's row 0
 
     char *mine = smem + warp * (kStages * Tile::kBytes);
-    const uint32_t mine_u32 = smem_u32(mine);
     const int32_t *table = p.block_table + b * p.table_stride;
-    uint32_t held = 0;  // bit s: stage s holds a tile that is there
 
-    auto page_of = [&](int tile) -> int32_t {
-        if (tile >= chunk_last) return -1;
-        return __ldg(table + static_cast<uint32_t>(tile * 16) / static_cast<uint32_t>(p.page_size));
-    };
-    auto issue = [&](int tile, int32_t page, int stage) {
-        held &= ~(1u << stage);
-        if (page >= 0 && page < p.num_pages) {
-            held |= 1u << stage;
-            const int off = static_cast<uint32_t>(tile * 16) % static_cast<uint32_t>(p.page_size);
-            const int64_t cell = (static_cast<int64_t>(page) * p.kv_heads + kvh) * p.page_size + off;
-            const uint32_t dst = mine_u32 + stage * Tile::kBytes;
-            const uint8_t *k = p.codes[0] + cell * (D / 2), *v = p.codes[1] + cell * (D / 2);
+    // This lane's pieces of a tile: 16 bytes of codes for every 32 lanes,
+    // [group][token][half] in shared memory (V's tokens in the order 0, 2, .. 14,
+    // 1, 3, ..), and one 16-byte piece of scales.
+    constexpr int kPieces = D / 32;  // of a token
+    const int token = lane / kPieces, part = lane % kPieces;
+    const uint32_t k_dst = smem_u32(mine) + (part / 2) * 512 + (part & 1) * 16 + token * 32;
+    const uint32_t v_dst = smem_u32(mine) + Tile::kCodes + (part / 2) * 512 + (part & 1) * 16 +
+                           (((token & 1) << 3) | (token >> 1)) * 32;
+    const int kv = lane / (Tile::kScales / 16);  // 0: K's scales, 1: V's, above: none
+    const uint32_t s_dst = smem_u32(mine) + 2 * Tile::kCodes + lane * 16;
+    const uint8_t *k_src = p.codes[0] + static_cast<int64_t>(kvh) * p.page_size * (D / 2) + lane * 16;
+    const uint8_t *v_src = p.codes[1] + static_cast<int64_t>(kvh) * p.page_size * (D / 2) + lane * 16;
+    const char *s_src = reinterpret_cast<const char *>(p.scales[kv & 1] + static_cast<int64_t>(kvh) * p.page_size * G) +
+                        (lane % (Tile::kScales / 16)) * 16;
+    const uint32_t page_codes = static_cast<uint32_t>(p.kv_heads) * p.page_size * (D / 2);
+    const uint32_t page_scales = static_cast<uint32_t>(p.kv_heads) * p.page_size * (G * 2);
+
+    // The tile to load next: its number, its page's place in the table, its
+    // place in the page, and the page, read one step ahead of the copy.
+    const uint32_t page_tiles = static_cast<uint32_t>(p.page_size) / 16;
+    const uint32_t step_pages = kAttnWarps / page_tiles, step_rest = kAttnWarps % page_tiles;
+    int load_tile = chunk_first + warp;
+    uint32_t load_page = static_cast<uint32_t>(load_tile) / page_tiles, load_off = static_cast<uint32_t>(load_tile) % page_tiles;
+    int32_t page = load_tile < chunk_last ? __ldg(table + load_page) : -1;
+    uint32_t held = 0;  // bit 0: the tile at hand is there, bit i: the i-th after it
+
+    auto issue = [&](int stage) {
+        const bool there = page >= 0 && page < p.num_pages;
+        held = (held >> 1) | (there ? 1u << (kStages - 1) : 0u);
+        if (there) {
+            const uint32_t at = stage * Tile::kBytes;
+            const uint64_t codes = static_cast<uint64_t>(static_cast<uint32_t>(page)) * page_codes + load_off * Tile::kCodes;
+            const uint64_t scales = static_cast<uint64_t>(static_cast<uint32_t>(page)) * page_scales + load_off * Tile::kScales;
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) {  // 16-byte pieces: [group][token][half], V's tokens 0, 2, .. 14, 1, 3, ..
-                const int piece = i * 32 + lane, token = piece / (D / 32), part = piece % (D / 32);
-                const uint32_t at = (part / 2) * 512 + (part & 1) * 16;
-                cp_async16(dst + at + token * 32, k + piece * 16);
-                cp_async16(dst + Tile::kCodes + at + (((token & 1) << 3) | (token >> 1)) * 32, v + piece * 16);
+            for (int i = 0; i < D / 64; ++i) {
+                cp_async16(k_dst + at + i * (32 / kPieces) * 32, k_src + codes + i * 512);
+                cp_async16(v_dst + at + i * (16 / kPieces) * 32, v_src + codes + i * 512);
             }
-            if (lane < 2 * (Tile::kScales / 16)) {
-                const int kv = lane >= Tile::kScales / 16, piece = lane - kv * (Tile::kScales / 16);
-                cp_async16(dst + 2 * Tile::kCodes + kv * Tile::kScales + piece * 16,
-                           reinterpret_cast<const char *>(p.scales[kv] + cell * G) + piece * 16);
-            }
+            if (kv < 2) cp_async16(s_dst + at, s_src + scales);
         }
         cp_commit();
+        load_tile += kAttnWarps;
+        load_page += step_pages;
+        load_off += step_rest;
+        if (load_off >= page_tiles) load_off -= page_tiles, ++load_page;
+        page = load_tile < chunk_last ? __ldg(table + load_page) : -1;
     };
 
-    int tile = chunk_first + warp;
-    int32_t page = page_of(tile);
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
-        const int32_t next = page_of(tile + (s + 1) * kAttnWarps);
-        issue(tile + s * kAttnWarps, page, s);
-        page = next;
-    }
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
 
     // Queries: this thread's B operands (row 8 j + g, dims 64 gr + 16 c .. + 15)
     // and, for its score columns 2c and 2c + 1, the row's factor and limits.
@@ -308,35 +327,33 @@ __global__ void __launch_bounds__(kAttnWarps * 32) kv4_attention_kernel(const __
     const int lowest = base_pos + r0 / p.group;                                    // the tile's first row
     const int highest = base_pos + (min(r0 + R, rows) - 1) / p.group;
 
+    // ref: kOffset - the rows' reference exponents (infinity: none yet; rows that see nothing need none)
     float o[NT][D / 16][4] = {};
-    float m[NT][2], l[NT][2];
+    float ref[NT][2], l[NT][2];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) m[j][0] = m[j][1] = -INFINITY, l[j][0] = l[j][1] = 0.0f;
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            ref[j][e] = r0 + 8 * j + 2 * c + e < rows && top[j][e] >= 0 ? INFINITY : kOffset;
+            l[j][e] = 0.0f;
+        }
+    bool unset = true;  // some row has no reference yet
 
     int stage = 0;
-    for (; tile < chunk_last; tile += kAttnWarps) {
-        {
-            const int ahead = tile + (kStages - 1) * kAttnWarps;
-            const int32_t next = page_of(ahead + kAttnWarps);
-            issue(ahead, page, (stage + kStages - 1) % kStages);
-            page = next;
-        }
+    for (int tile = chunk_first + warp; tile < chunk_last; tile += kAttnWarps) {
+        issue(stage == 0 ? kStages - 1 : stage - 1);
         cp_wait<kStages - 1>();
         __syncwarp();
-        if (held & (1u << stage)) {
+        if (held & 1u) {
             const char *kc = mine + stage * Tile::kBytes, *vc = kc + Tile::kCodes;
             const __half *ks = reinterpret_cast<const __half *>(kc + 2 * Tile::kCodes);
             const __half *vs = ks + 16 * G;
             float s[NT][4];
-            float vscale[G][2];
-            float lv[2];
 #pragma unroll
             for (int gr = 0; gr < G; ++gr) {
                 const uint2 ka = *reinterpret_cast<const uint2 *>(kc + gr * 512 + g * 32 + c * 8);
                 const uint2 kb = *reinterpret_cast<const uint2 *>(kc + gr * 512 + (g + 8) * 32 + c * 8);
                 const float sa = __half2float(ks[g * G + gr]), sb = __half2float(ks[(g + 8) * G + gr]);
-                vscale[gr][0] = __half2float(vs[g * G + gr]);
-                vscale[gr][1] = __half2float(vs[(g + 8) * G + gr]);
                 uint32_t a[2][4], bq[2][4];
                 codes8(ka.x, a[0]);
                 codes8(ka.y, a[1]);
@@ -344,61 +361,83 @@ __global__ void __launch_bounds__(kAttnWarps * 32) kv4_attention_kernel(const __
                 codes8(kb.y, bq[1]);
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    float acc[4];
+                    mma16816_first(acc, a[0][0], bq[0][0], a[0][1], bq[0][1], q[j][gr][0], q[j][gr][1]);
 #pragma unroll
                     for (int w = 0; w < 2; ++w)
 #pragma unroll
-                        for (int i = 0; i < 4; i += 2)
+                        for (int i = w == 0 ? 2 : 0; i < 4; i += 2)
                             mma16816(acc, a[w][i], bq[w][i], a[w][i + 1], bq[w][i + 1], q[j][gr][4 * w + i],
                                      q[j][gr][4 * w + i + 1]);
-                    if (gr == 0) {
-                        s[j][0] = acc[0] * sa;
-                        s[j][1] = acc[1] * sa;
-                        s[j][2] = acc[2] * sb;
-                        s[j][3] = acc[3] * sb;
-                    } else {
-                        s[j][0] = fmaf(acc[0], sa, s[j][0]);
-                        s[j][1] = fmaf(acc[1], sa, s[j][1]);
-                        s[j][2] = fmaf(acc[2], sb, s[j][2]);
-                        s[j][3] = fmaf(acc[3], sb, s[j][3]);
-                    }
+                    s[j][0] = gr == 0 ? acc[0] * sa : fmaf(acc[0], sa, s[j][0]);
+                    s[j][1] = gr == 0 ? acc[1] * sa : fmaf(acc[1], sa, s[j][1]);
+                    s[j][2] = gr == 0 ? acc[2] * sb : fmaf(acc[2], sb, s[j][2]);
+                    s[j][3] = gr == 0 ? acc[3] * sb : fmaf(acc[3], sb, s[j][3]);
                 }
             }
-            // log2 of each token's largest value scale, kept to what halves can hold
+            float vscale[G][2];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                float v = vscale[0][t];
-#pragma unroll
-                for (int gr = 1; gr < G; ++gr) v = fmaxf(v, vscale[gr][t]);
-                lv[t] = fminf(fmaxf(lg2(v), -24.0f), 16.0f);
+            for (int gr = 0; gr < G; ++gr) {
+                vscale[gr][0] = __half2float(vs[g * G + gr]);
+                vscale[gr][1] = __half2float(vs[(g + 8) * G + gr]);
             }
             const int t0 = tile * 16;
             const bool masked = t0 + 15 > lowest || (p.window > 0 && t0 <= highest - p.window);
-            bool grow = false;
+            float w[NT][4], x[NT][G][4];
+            auto weigh = [&](int j, int e, bool hide) {
+                w[j][e] = hide ? 0.0f : ex2(fmaf(s[j][e], qmul[j][e & 1], ref[j][e & 1]));
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr)  // a hidden token's scale may be anything
+                    x[j][gr][e] = hide ? 0.0f : w[j][e] * vscale[gr][e >> 1];
+            };
+            uint32_t hidden = 0;  // bit 4 j + e: weight e of query tile j
+            if (masked) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int t = t0 + g + (e & 2) * 4, pos = top[j][e & 1];
+                        const bool hide = t > pos || (p.window > 0 && t <= pos - p.window);
+                        hidden |= hide ? 1u << (4 * j + e) : 0u;
+                        weigh(j, e, hide);
+                    }
+            } else {
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) weigh(j, e, false);
+            }
+            float big = 0.0f;
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[j][e] *= qmul[j][e & 1];
-                    if (masked) {
-                        const int t = t0 + g + (e & 2) * 4;
-                        const int pos = top[j][e & 1];
-                        if (t > pos || (p.window > 0 && t <= pos - p.window)) s[j][e] = -INFINITY;
-                    }
-                    grow |= s[j][e] + lv[e >> 1] > m[j][e & 1] + kGrow;
+                for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) big = fmaxf(big, x[j][gr][e]);
+            const bool over = big > kLargest;
+            if (unset || __any_sync(0xFFFFFFFFu, over)) {
+                float lv[2];  // log2 of each token's largest value scale, kept to what halves can hold
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    float v = vscale[0][t];
+#pragma unroll
+                    for (int gr = 1; gr < G; ++gr) v = fmaxf(v, vscale[gr][t]);
+                    lv[t] = fminf(fmaxf(lg2(v), -24.0f), 16.0f);
                 }
-            if (__any_sync(0xFFFFFFFFu, grow)) {
+                bool none = false;
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float x = fmaxf(s[j][e] + lv[0], s[j][e + 2] + lv[1]);
-                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
-                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
-                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-                        const float mn = fmaxf(m[j][e], x);
-                        const float f = mn == m[j][e] ? 1.0f : ex2(m[j][e] - mn);
-                        m[j][e] = mn;
+                        float y = hidden >> (4 * j + e) & 1u ? -INFINITY : fmaf(s[j][e], qmul[j][e], lv[0]);
+                        y = fmaxf(y, hidden >> (4 * j + e + 2) & 1u ? -INFINITY : fmaf(s[j][e + 2], qmul[j][e], lv[1]));
+                        y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 4));
+                        y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 8));
+                        y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 16));
+                        const float r = fminf(ref[j][e], kOffset - y);
+                        const float f = r == ref[j][e] ? 1.0f : ex2(r - ref[j][e]);
+                        ref[j][e] = r;
+                        none |= r == INFINITY;
                         l[j][e] *= f;
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i) {
@@ -406,30 +445,21 @@ __global__ void __launch_bounds__(kAttnWarps * 32) kv4_attention_kernel(const __
                             o[j][i][e + 2] *= f;
                         }
                     }
+                unset = __any_sync(0xFFFFFFFFu, none);
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) weigh(j, e, hidden >> (4 * j + e) & 1u);
             }
             uint32_t pb[NT][G][2];
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                float w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float ref = m[j][e & 1] == -INFINITY ? 0.0f : m[j][e & 1];
-                    w[e] = ex2(s[j][e] - ref + kOffset);
-                }
-                l[j][0] += w[0] + w[2];
-                l[j][1] += w[1] + w[3];
+                l[j][0] += w[j][0] + w[j][2];
+                l[j][1] += w[j][1] + w[j][3];
 #pragma unroll
                 for (int gr = 0; gr < G; ++gr) {
-                    float x[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[e] = w[e] * vscale[gr][e >> 1];
-                    if (masked) {  // a masked token's scale may be anything
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (w[e] == 0.0f) x[e] = 0.0f;
-                    }
-                    pb[j][gr][0] = transpose8x8(pack_half2(x[0], x[1]));
-                    pb[j][gr][1] = transpose8x8(pack_half2(x[2], x[3]));
+                    pb[j][gr][0] = transpose8x8(pack_half2(x[j][gr][0], x[j][gr][1]));
+                    pb[j][gr][1] = transpose8x8(pack_half2(x[j][gr][2], x[j][gr][3]));
                 }
             }
 #pragma unroll
@@ -455,14 +485,14 @@ __global__ void __launch_bounds__(kAttnWarps * 32) kv4_attention_kernel(const __
             }
         }
         __syncwarp();
-        stage = (stage + 1) % kStages;
+        stage = stage + 1 == kStages ? 0 : stage + 1;
     }
     cp_wait<0>();
     __syncwarp();
 
     // Join the warps: O, the exponent m - kOffset and l of each row, in shared memory.
-    float *part = reinterpret_cast<float *>(mine);
-    float *stat = part + R * D;
+    float *joined = reinterpret_cast<float *>(mine);
+    float *stat = joined + R * D;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -473,10 +503,10 @@ __global__ void __launch_bounds__(kAttnWarps * 32) kv4_attention_kernel(const __
             const int r = 8 * j + 2 * c + e;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i)  // dims 64 gr + 8 g + 2 (i % 4), + 1
-                *reinterpret_cast<float2 *>(part + r * D + (i / 4) * 64 + g * 8 + (i % 4) * 2) =
+                *reinterpret_cast<float2 *>(joined + r * D + (i / 4) * 64 + g * 8 + (i % 4) * 2) =
                     make_float2(o[j][i][e], o[j][i][e + 2]);
-            if (g == 0) {
-                stat[r] = m[j][e] == -INFINITY ? (l[j][e] == 0.0f ? -INFINITY : -kOffset) : m[j][e] - kOffset;
+            if (g == 0) {  // a row whose scores are all NaN has no reference: its sum carries the NaN
+                stat[r] = l[j][e] == 0.0f ? -INFINITY : (ref[j][e] == INFINITY ? 0.0f : -ref[j][e]);
                 stat[R + r] = l[j][e];
             }
         }
@@ -510,20 +540,22 @@ __global__ void __launch_bounds__(kAttnWarps * 32) kv4_attention_kernel(const __
             *reinterpret_cast<float4 *>(p.part_o + cell * D + d) = sum;
             if (d == 0) reinterpret_cast<float2 *>(p.part_s)[cell] = make_float2(top_m, total);
         } else {
-            store_row<E>(p, row, head * D + d, sum, total);
+            store_row<E>(p, row, static_cast<int64_t>(head) * D + d, sum, total);
             if (d == 0 && p.lse) p.lse[row * p.q_heads + head] = finish_lse(top_m, total);
         }
     }
 }
 
-// Joins the chunks of each row: one warp per row and query head.
+// Joins the chunks of each row: one CTA per row and query head, its warps taking
+// the chunks in turn (a long cache has many more chunks than rows).
+constexpr int kJoinWarps = 4;
 template <typename E, int D>
-__global__ void __launch_bounds__(128) kv4_join_kernel(const __grid_constant__ Kv4AttnParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const __grid_constant__ Kv4AttnParams p) {
     pdl_wait_and_release();
-    const int lane = threadIdx.x & 31;
+    __shared__ float held[kJoinWarps][D + 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Seq seq = sequence(p, blockIdx.y);
-    const int item = static_cast<int>(blockIdx.x) * 4 + static_cast<int>(threadIdx.x >> 5);
-    const int i = item / p.q_heads, head = item % p.q_heads;
+    const int i = static_cast<int>(blockIdx.x) / p.q_heads, head = static_cast<int>(blockIdx.x) % p.q_heads;
     if (i >= seq.rows) return;
     const int64_t row = seq.row0 + i;
     const int tile_rows = 8 * p.n_tiles;
@@ -536,31 +568,37 @@ __global__ void __launch_bounds__(128) kv4_join_kernel(const __grid_constant__ K
     for (int k = lane; k < n; k += 32) top_m = fmaxf(top_m, stat[k].x);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) top_m = fmaxf(top_m, __shfl_xor_sync(0xFFFFFFFFu, top_m, off));
-    constexpr int N = D / 128 > 0 ? D / 128 : 1;
-    float4 sum[N];
-#pragma unroll
-    for (int e = 0; e < N; ++e) sum[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    constexpr int N = D / 32;
+    float sum[N] = {};
     float total = 0.0f;
-    const int d0 = lane * 4;
 #pragma unroll 4
-    for (int k = 0; k < n; ++k) {
+    for (int k = warp; k < n; k += kJoinWarps) {
         const float2 st = stat[k];
         const float f = st.x == -INFINITY ? 0.0f : ex2(st.x - top_m);
         total = fmaf(st.y, f, total);
+        const float *o = p.part_o + (cell + k) * D + lane;
 #pragma unroll
-        for (int e = 0; e < N; ++e)
-            if (d0 + e * 128 < D) {
-                const float4 v = *reinterpret_cast<const float4 *>(p.part_o + (cell + k) * D + d0 + e * 128);
-                sum[e].x = fmaf(v.x, f, sum[e].x);
-                sum[e].y = fmaf(v.y, f, sum[e].y);
-                sum[e].z = fmaf(v.z, f, sum[e].z);
-                sum[e].w = fmaf(v.w, f, sum[e].w);
-            }
+        for (int e = 0; e < N; ++e) sum[e] = fmaf(o[32 * e], f, sum[e]);
     }
 #pragma unroll
-    for (int e = 0; e < N; ++e)
-        if (d0 + e * 128 < D) store_row<E>(p, row, head * D + d0 + e * 128, sum[e], total);
-    if (lane == 0 && p.lse) p.lse[row * p.q_heads + head] = finish_lse(top_m, total);
+    for (int e = 0; e < N; ++e) held[warp][lane + 32 * e] = sum[e];
+    if (lane == 0) held[warp][D] = total;
+    __syncthreads();
+    if (threadIdx.x < D / 4) {
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float all = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            const float *h = held[w] + threadIdx.x * 4;
+            v.x += h[0];
+            v.y += h[1];
+            v.z += h[2];
+            v.w += h[3];
+            all += held[w][D];
+        }
+        store_row<E>(p, row, static_cast<int64_t>(head) * D + threadIdx.x * 4, v, all);
+        if (threadIdx.x == 0 && p.lse) p.lse[row * p.q_heads + head] = finish_lse(top_m, all);
+    }
 }
 
 using namespace checks;
@@ -580,7 +618,7 @@ Plan plan(int32_t B, int32_t q_heads, int32_t kv_heads, int32_t max_q_len, int32
     const int64_t units = (int64_t)(B < 1 ? 1 : B) * kv_heads * tiles;
     const int64_t len_tiles = ((int64_t)max_seq_len + 15) / 16;
     // chunks of at least 256 tokens, as many as give every SM several
-    int64_t want = (4 * kSlots + units - 1) / units;
+    int64_t want = (2 * kSlots + units - 1) / units;
     int64_t chunk = (len_tiles + want - 1) / want;
     if (chunk < 16) chunk = 16;
     pl.chunk_tiles = (int32_t)chunk;
@@ -600,7 +638,7 @@ qkn_status launch_attention(const Kv4AttnParams &p, dim3 grid, dim3 join_grid, v
     }
     qkn_status st = launched(launch_pdl(fn, grid, kAttnWarps * 32, smem, stream, p));
     if (st != QKN_OK || p.splits == 1) return st;
-    return launched(launch_pdl((const void *)kv4_join_kernel<E, D>, join_grid, 128, 0, stream, p));
+    return launched(launch_pdl((const void *)kv4_join_kernel<E, D>, join_grid, kJoinWarps * 32, 0, stream, p));
 }
 template <typename E>
 qkn_status launch_attention(const Kv4AttnParams &p, int d, dim3 grid, dim3 join_grid, void *stream) {
@@ -721,7 +759,7 @@ qkn_status qknorm_kv4_attention(const void *q, int64_t q_stride, void *out, int6
     p.part_o = static_cast<float *>(workspace);
     p.part_s = p.part_o + T * q_heads * pl.splits * head_dim;
     const dim3 grid((unsigned)pl.splits, (unsigned)(pl.row_tiles * kv_heads), (unsigned)B);
-    const dim3 join_grid((unsigned)(((int64_t)max_q_len * q_heads + 3) / 4), (unsigned)B);
+    const dim3 join_grid((unsigned)(max_q_len * q_heads), (unsigned)B);
     return dtype == QKN_BF16 ? launch_attention<__nv_bfloat16>(p, head_dim, grid, join_grid, stream)
                              : launch_attention<__half>(p, head_dim, grid, join_grid, stream);
 }
