@@ -34,8 +34,11 @@ struct Kv4AttnParams {
     float scale;
     int32_t q_vector, out_vector;  // rows move as 16-byte (8-byte) vectors
     int32_t n_tiles;               // query tile: 8 * n_tiles rows
-    int32_t chunk_tiles, splits;   // 16-token tiles of a chunk, chunks at most
-    float *part_o, *part_s;        // [T][q_heads][splits][head_dim] and (exponent, sum) pairs
+    int32_t row_tiles;             // query tiles of a sequence at most
+    int32_t shared;                // whether units are cut at the CTAs' shares (else one CTA per unit)
+    float *part_o;                 // shared: [grid][2][rows of a tile][head_dim], partial outputs
+    float2 *part_s;                // and their (exponent, sum) pairs
+    int64_t *starts;               // [B * row_tiles] first tile of each sequence and query tile, then the share
 };
 
 // Rows and cached tokens of sequence b, kept inside the buffers.
@@ -79,10 +82,13 @@ __device__ __forceinline__ float finish_lse(float m, float total) {  // base 2 -
 }
 
 // ----------------------------------------------------------------------------
-// One CTA takes a tile of 8 * NT query rows (rows of one sequence that read the
-// same KV head: row r = token r / group, head r % group) and a chunk of the
-// sequence's tokens; its warps take the chunk's 16-token tiles in turn, each
-// with its own running maximum, sum and output, joined once at the end.
+// A unit is a tile of 8 * NT query rows of one sequence that read the same KV
+// head (row r = token r / group, head r % group) with the 16-token tiles they
+// see.  With many units or short sequences a CTA takes one; otherwise all units'
+// tiles, end to end, are cut into equal shares, one per resident CTA, whatever
+// the sequences' lengths, and a unit that a cut goes through is joined by a
+// second launch.  A CTA's warps take a unit's tiles in turn, each with its own
+// running maximum, sum and output, joined at the end of the unit.
 //
 // Scores are formed transposed, S^T = K Q^T, and so is the output, O^T = V^T P^T,
 // with mma.m16n8k16: the 16 rows are cached tokens (or value dims), the 8
@@ -105,6 +111,7 @@ __device__ __forceinline__ float finish_lse(float m, float total) {  // base 2 -
 // vote per tile); the exact maximum is not needed, as l and O share it.
 constexpr int kAttnWarps = 4;
 constexpr int kStages = 4;
+constexpr int kLeastShare = 16;  // tiles: 4 for each warp
 constexpr float kOffset = 7.0f, kLargest = 32768.0f;
 
 template <int D>
@@ -193,20 +200,13 @@ __device__ __forceinline__ TileRange tile_range(const Kv4AttnParams &p, const Se
 }
 
 template <typename E, int D, int NT>
-__global__ void __launch_bounds__(kAttnWarps * 32) kv4_attention_kernel(const __grid_constant__ Kv4AttnParams p) {
+__device__ __forceinline__ void attend_unit(const Kv4AttnParams &p, const Seq &seq, int b, int kvh, int r0, int chunk_first,
+                                            int chunk_last, int slot) {
     using Tile = Kv4Tile<D>;
     constexpr int G = Tile::kGroups, R = 8 * NT;
     extern __shared__ __align__(128) char smem[];
-    pdl_wait_and_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-    const int b = blockIdx.z, kvh = blockIdx.y % p.kv_heads, r0 = static_cast<int>(blockIdx.y / p.kv_heads) * R;
-    const Seq seq = sequence(p, b);
     const int rows = seq.rows * p.group;
-    if (r0 >= rows) return;
-    const TileRange range = tile_range(p, seq, r0, R);
-    const int chunk_first = range.first + static_cast<int>(blockIdx.x) * p.chunk_tiles;
-    if (blockIdx.x > 0 && chunk_first >= range.last) return;  // chunk 0 also answers for rows without tokens
-    const int chunk_last = min(chunk_first + p.chunk_tiles, range.last);
     const int base_pos = seq.len - seq.rows;  // position of the sequence's row 0
 
     char *mine = smem + warp * (kStages * Tile::kBytes);
@@ -259,7 +259,6 @@ __global__ void __launch_bounds__(kAttnWarps * 32) kv4_attention_kernel(const __
         if (load_off >= page_tiles) load_off -= page_tiles, ++load_page;
         page = load_tile < chunk_last ? __ldg(table + load_page) : -1;
     };
-
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) issue(i);
 
@@ -535,10 +534,10 @@ __global__ void __launch_bounds__(kAttnWarps * 32) kv4_attention_kernel(const __
         }
         const int64_t row = seq.row0 + (r0 + r) / p.group;
         const int head = kvh * p.group + (r0 + r) % p.group;
-        if (p.splits > 1) {
-            const int64_t cell = (row * p.q_heads + head) * p.splits + blockIdx.x;
+        if (slot >= 0) {
+            const int64_t cell = static_cast<int64_t>(slot) * R + r;
             *reinterpret_cast<float4 *>(p.part_o + cell * D + d) = sum;
-            if (d == 0) reinterpret_cast<float2 *>(p.part_s)[cell] = make_float2(top_m, total);
+            if (d == 0) p.part_s[cell] = make_float2(top_m, total);
         } else {
             store_row<E>(p, row, static_cast<int64_t>(head) * D + d, sum, total);
             if (d == 0 && p.lse) p.lse[row * p.q_heads + head] = finish_lse(top_m, total);
@@ -546,26 +545,125 @@ __global__ void __launch_bounds__(kAttnWarps * 32) kv4_attention_kernel(const __
     }
 }
 
-// Joins the chunks of each row: one CTA per row and query head, its warps taking
-// the chunks in turn (a long cache has many more chunks than rows).
+// Tiles of sequence b's query tile rt: at least one for rows that exist (a row
+// without tokens is still answered), times the KV heads.
+__device__ __forceinline__ int64_t pair_tiles(const Kv4AttnParams &p, int b, int rt, int tile_rows) {
+    const Seq s = sequence(p, b);
+    if (rt * tile_rows >= s.rows * p.group) return 0;
+    const TileRange t = tile_range(p, s, rt * tile_rows, tile_rows);
+    return static_cast<int64_t>(max(t.last - t.first, 1)) * p.kv_heads;
+}
+
+// This CTA's share of all units' tiles: [first, last), and the (sequence, query
+// tile) pair it begins in, `at` tiles into it.
+struct Share {
+    int64_t tiles, at;
+    int pair;
+};
+__device__ __forceinline__ Share find_share(const Kv4AttnParams &p, int tile_rows) {
+    __shared__ int64_t sums[kAttnWarps];
+    __shared__ Share found;
+    const int n = p.B * p.row_tiles, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int slice = (n + kAttnWarps * 32 - 1) / (kAttnWarps * 32);
+    const int i0 = min(static_cast<int>(threadIdx.x) * slice, n), i1 = min(i0 + slice, n);
+    int64_t sum = 0;
+    for (int i = i0; i < i1; ++i) sum += pair_tiles(p, i / p.row_tiles, i % p.row_tiles, tile_rows);
+    int64_t before = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, before, off);
+        if (lane >= off) before += v;
+    }
+    if (lane == 31) sums[warp] = before;
+    __syncthreads();
+    int64_t total = 0;
+    before -= sum;
+    for (int w = 0; w < kAttnWarps; ++w) {
+        if (w < warp) before += sums[w];
+        total += sums[w];
+    }
+    const int64_t share = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kLeastShare));
+    const int64_t first = share * blockIdx.x;
+    if (threadIdx.x == 0) found = Share{0, 0, 0};
+    __syncthreads();
+    const bool mine = first >= before && first < before + sum;
+    if (blockIdx.x == 0 || mine) {
+        int64_t at = before;
+        for (int i = i0; i < i1; ++i) {
+            const int64_t c = pair_tiles(p, i / p.row_tiles, i % p.row_tiles, tile_rows);
+            if (blockIdx.x == 0) p.starts[i] = at;
+            if (first >= at && first < at + c) found = Share{min(share, total - first), first - at, i};
+            at += c;
+        }
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.starts[n] = share;
+    __syncthreads();
+    return found;
+}
+
+// CTAs resident on an SM: what 64 K registers hold.
+template <int D, int NT>
+constexpr int kResident = D == 64 ? (NT == 1 ? 6 : 4) : D == 128 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 3 : 2);
+
+template <typename E, int D, int NT>
+__global__ void __launch_bounds__(kAttnWarps * 32, kResident<D, NT>) kv4_attention_kernel(const __grid_constant__ Kv4AttnParams p) {
+    constexpr int R = 8 * NT;
+    pdl_wait_and_release();
+    if (!p.shared) {
+        const int rt = blockIdx.x / p.kv_heads, kvh = blockIdx.x % p.kv_heads, b = blockIdx.y;
+        const Seq seq = sequence(p, b);
+        if (rt * R >= seq.rows * p.group) return;
+        const TileRange range = tile_range(p, seq, rt * R, R);
+        attend_unit<E, D, NT>(p, seq, b, kvh, rt * R, range.first, range.last, -1);
+        return;
+    }
+    Share mine = find_share(p, R);
+    for (int pair = mine.pair; mine.tiles > 0; ++pair) {
+        const int b = pair / p.row_tiles, r0 = pair % p.row_tiles * R;
+        if (b >= p.B) return;
+        const Seq seq = sequence(p, b);
+        if (r0 >= seq.rows * p.group) continue;
+        const TileRange range = tile_range(p, seq, r0, R);
+        const int count = max(range.last - range.first, 1);
+        for (int kvh = static_cast<int>(mine.at / count); kvh < p.kv_heads && mine.tiles > 0; ++kvh) {
+            const int skip = static_cast<int>(mine.at - static_cast<int64_t>(kvh) * count);
+            const int take = static_cast<int>(min(static_cast<int64_t>(count - skip), mine.tiles));
+            // a CTA has at most one unit that it only ends (or passes through) and one that it only begins
+            const int slot = take == count ? -1 : static_cast<int>(blockIdx.x) * 2 + (skip == 0 ? 1 : 0);
+            attend_unit<E, D, NT>(p, seq, b, kvh, r0, range.first + skip, min(range.first + skip + take, range.last), slot);
+            __syncthreads();  // the ring is written again
+            mine.tiles -= take;
+            mine.at += take;
+        }
+        mine.at = 0;
+    }
+}
+
+// Joins the units that the shares cut: one CTA per unit and row, its warps
+// taking the partial results in turn.
 constexpr int kJoinWarps = 4;
 template <typename E, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const __grid_constant__ Kv4AttnParams p) {
     pdl_wait_and_release();
     __shared__ float held[kJoinWarps][D + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Seq seq = sequence(p, blockIdx.y);
-    const int i = static_cast<int>(blockIdx.x) / p.q_heads, head = static_cast<int>(blockIdx.x) % p.q_heads;
-    if (i >= seq.rows) return;
-    const int64_t row = seq.row0 + i;
-    const int tile_rows = 8 * p.n_tiles;
-    const int r = i * p.group + head % p.group;
-    const TileRange range = tile_range(p, seq, r / tile_rows * tile_rows, tile_rows);
-    const int n = max(1, (range.last - range.first + p.chunk_tiles - 1) / p.chunk_tiles);
-    const int64_t cell = (row * p.q_heads + head) * p.splits;
-    const float2 *stat = reinterpret_cast<const float2 *>(p.part_s) + cell;
+    const int pair = static_cast<int>(blockIdx.x) / p.kv_heads, kvh = static_cast<int>(blockIdx.x) % p.kv_heads;
+    const int tile_rows = 8 * p.n_tiles, r0 = pair % p.row_tiles * tile_rows;
+    const Seq seq = sequence(p, pair / p.row_tiles);
+    const int r = r0 + static_cast<int>(blockIdx.y);
+    if (r >= seq.rows * p.group) return;
+    const TileRange range = tile_range(p, seq, r0, tile_rows);
+    const int count = max(range.last - range.first, 1);
+    const int64_t share = p.starts[p.B * p.row_tiles], start = p.starts[pair] + static_cast<int64_t>(kvh) * count;
+    const int64_t cta0 = start / share;
+    const int n = static_cast<int>((start + count - 1) / share - cta0) + 1;
+    if (n == 1) return;
+    const int64_t row = seq.row0 + r / p.group;
+    const int head = kvh * p.group + r % p.group;
+    // partial k: the first CTA's begun unit, then the later ones' ended (or passed) unit
+    auto cell_of = [&](int k) -> int64_t { return ((cta0 + k) * 2 + (k == 0 ? 1 : 0)) * tile_rows + blockIdx.y; };
     float top_m = -INFINITY;
-    for (int k = lane; k < n; k += 32) top_m = fmaxf(top_m, stat[k].x);
+    for (int k = lane; k < n; k += 32) top_m = fmaxf(top_m, p.part_s[cell_of(k)].x);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) top_m = fmaxf(top_m, __shfl_xor_sync(0xFFFFFFFFu, top_m, off));
     constexpr int N = D / 32;
@@ -573,10 +671,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const __grid_
     float total = 0.0f;
 #pragma unroll 4
     for (int k = warp; k < n; k += kJoinWarps) {
-        const float2 st = stat[k];
+        const int64_t cell = cell_of(k);
+        const float2 st = p.part_s[cell];
         const float f = st.x == -INFINITY ? 0.0f : ex2(st.x - top_m);
         total = fmaf(st.y, f, total);
-        const float *o = p.part_o + (cell + k) * D + lane;
+        const float *o = p.part_o + cell * D + lane;
 #pragma unroll
         for (int e = 0; e < N; ++e) sum[e] = fmaf(o[32 * e], f, sum[e]);
     }
@@ -604,26 +703,28 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const __grid_
 using namespace checks;
 
 // How a call is cut up, from sizes the host knows.
-struct Plan {
-    int32_t n_tiles, row_tiles, chunk_tiles, splits;
-};
-constexpr int64_t kSlots = 148 * 4;  // resident CTAs on a B200
+constexpr int64_t kMaxRows = 1 << 20;  // max_q_len * q_heads
 
-Plan plan(int32_t B, int32_t q_heads, int32_t kv_heads, int32_t max_q_len, int32_t max_seq_len) {
+struct Plan {
+    int32_t n_tiles, row_tiles;
+    int32_t ctas;  // shares (0: one CTA per unit)
+    int64_t pairs;
+};
+constexpr int kSms = 148;
+
+Plan plan(int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t max_q_len, int32_t max_seq_len) {
     Plan pl{};
     const int64_t rows = (int64_t)max_q_len * (q_heads / kv_heads);
     pl.n_tiles = rows <= 8 ? 1 : 2;
-    const int64_t tiles = (rows + 8 * pl.n_tiles - 1) / (8 * pl.n_tiles);
-    pl.row_tiles = tiles > INT32_MAX ? INT32_MAX : (int32_t)tiles;
-    const int64_t units = (int64_t)(B < 1 ? 1 : B) * kv_heads * tiles;
-    const int64_t len_tiles = ((int64_t)max_seq_len + 15) / 16;
-    // chunks of at least 256 tokens, as many as give every SM several
-    int64_t want = (2 * kSlots + units - 1) / units;
-    int64_t chunk = (len_tiles + want - 1) / want;
-    if (chunk < 16) chunk = 16;
-    pl.chunk_tiles = (int32_t)chunk;
-    pl.splits = (int32_t)((len_tiles + chunk - 1) / chunk);
-    if (pl.splits < 1) pl.splits = 1;
+    pl.row_tiles = (int32_t)((rows + 8 * pl.n_tiles - 1) / (8 * pl.n_tiles));
+    pl.pairs = (int64_t)B * pl.row_tiles;
+    const int64_t units = pl.pairs * kv_heads, tiles = ((int64_t)max_seq_len + 15) / 16;
+    const int resident = pl.n_tiles == 1 ? (head_dim == 64 ? kResident<64, 1> : head_dim == 128 ? kResident<128, 1> : kResident<256, 1>)
+                                         : (head_dim == 64 ? kResident<64, 2> : head_dim == 128 ? kResident<128, 2> : kResident<256, 2>);
+    const int64_t slots = (int64_t)kSms * resident;
+    if (units >= 4 * slots || tiles <= 2 * kLeastShare) return pl;
+    const int64_t most = (units * tiles + kLeastShare - 1) / kLeastShare;
+    pl.ctas = (int32_t)(most < slots ? most : slots);
     return pl;
 }
 
@@ -637,7 +738,7 @@ qkn_status launch_attention(const Kv4AttnParams &p, dim3 grid, dim3 join_grid, v
         if (e != cudaSuccess) return launched(e);
     }
     qkn_status st = launched(launch_pdl(fn, grid, kAttnWarps * 32, smem, stream, p));
-    if (st != QKN_OK || p.splits == 1) return st;
+    if (st != QKN_OK || !p.shared) return st;
     return launched(launch_pdl((const void *)kv4_join_kernel<E, D>, join_grid, kJoinWarps * 32, 0, stream, p));
 }
 template <typename E>
@@ -664,8 +765,10 @@ int64_t qknorm_kv4_attention_workspace_bytes(int64_t T, int32_t B, int32_t q_hea
     if (T < 0 || B < 0 || q_heads < 1 || kv_heads < 1 || head_dim < 1 || max_q_len < 1 || max_seq_len < 0 ||
         q_heads % kv_heads != 0 || head_dim > kRopeMaxHeadDim || T >= ((int64_t)1 << 31) / q_heads)
         return -1;
-    const Plan pl = plan(B, q_heads, kv_heads, max_q_len, max_seq_len);
-    return pl.splits == 1 ? 0 : T * q_heads * pl.splits * (head_dim + 2) * 4;
+    if ((int64_t)max_q_len * q_heads > kMaxRows) return -1;
+    const Plan pl = plan(B, q_heads, kv_heads, head_dim, max_q_len, max_seq_len);
+    // partial outputs and sums of every share's two ends, the pairs' first tiles
+    return pl.ctas == 0 ? 0 : (int64_t)pl.ctas * 2 * 8 * pl.n_tiles * (head_dim + 2) * 4 + (pl.pairs + 1) * 8;
 }
 
 qkn_status qknorm_kv4_attention(const void *q, int64_t q_stride, void *out, int64_t out_stride, float *lse,
@@ -700,15 +803,15 @@ qkn_status qknorm_kv4_attention(const void *q, int64_t q_stride, void *out, int6
         return fail(QKN_ERR_INVALID_ARG, "null pointer");
     if (((uintptr_t)q | (uintptr_t)out) & 1u || ((uintptr_t)lse | (uintptr_t)block_table | (uintptr_t)seq_lens | (uintptr_t)q_start) & 3u)
         return fail(QKN_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+    if ((int64_t)max_q_len * q_heads > kMaxRows)
+        return fail(QKN_ERR_UNSUPPORTED, "max_q_len = %d too long: call in chunks of rows", max_q_len);
     const int64_t need = qknorm_kv4_attention_workspace_bytes(T, B, q_heads, kv_heads, head_dim, max_q_len, max_seq_len);
     if (need < 0) return fail(QKN_ERR_INVALID_ARG, "sizes out of range");
     if (workspace_bytes < need || (need > 0 && !workspace))
         return fail(QKN_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)need);
     if (need > 0 && !aligned16(workspace)) return fail(QKN_ERR_INVALID_ARG, "the workspace must be 16-byte aligned");
     if (T == 0 || B == 0) return ok();
-    const Plan pl = plan(B, q_heads, kv_heads, max_q_len, max_seq_len);
-    if ((int64_t)max_q_len * q_heads > (1 << 20) || (int64_t)pl.row_tiles * kv_heads > 65535)
-        return fail(QKN_ERR_UNSUPPORTED, "max_q_len = %d too long: call in chunks", max_q_len);
+    const Plan pl = plan(B, q_heads, kv_heads, head_dim, max_q_len, max_seq_len);
     Span w[3], r[8];
     int nw = 0, nr = 0;
     w[nw++] = Span{out, width * 2, out_stride * 2, T, "out"};
@@ -754,12 +857,17 @@ qkn_status qknorm_kv4_attention(const void *q, int64_t q_stride, void *out, int6
     p.q_vector = aligned16(q) && p.q_stride % 16 == 0;
     p.out_vector = ((uintptr_t)out & 7u) == 0 && p.out_stride % 8 == 0;
     p.n_tiles = pl.n_tiles;
-    p.chunk_tiles = pl.chunk_tiles;
-    p.splits = pl.splits;
-    p.part_o = static_cast<float *>(workspace);
-    p.part_s = p.part_o + T * q_heads * pl.splits * head_dim;
-    const dim3 grid((unsigned)pl.splits, (unsigned)(pl.row_tiles * kv_heads), (unsigned)B);
-    const dim3 join_grid((unsigned)(max_q_len * q_heads), (unsigned)B);
+    p.row_tiles = pl.row_tiles;
+    p.shared = pl.ctas > 0;
+    if (p.shared) {
+        const int64_t cells = (int64_t)pl.ctas * 2 * 8 * pl.n_tiles;
+        p.part_o = static_cast<float *>(workspace);
+        p.part_s = reinterpret_cast<float2 *>(p.part_o + cells * head_dim);
+        p.starts = reinterpret_cast<int64_t *>(p.part_s + cells);
+    }
+    const int64_t tile_rows = 8 * pl.n_tiles, rows = (int64_t)max_q_len * p.group;
+    const dim3 grid = p.shared ? dim3((unsigned)pl.ctas) : dim3((unsigned)(pl.row_tiles * kv_heads), (unsigned)B);
+    const dim3 join_grid((unsigned)(pl.pairs * kv_heads), (unsigned)(rows < tile_rows ? rows : tile_rows));
     return dtype == QKN_BF16 ? launch_attention<__nv_bfloat16>(p, head_dim, grid, join_grid, stream)
                              : launch_attention<__half>(p, head_dim, grid, join_grid, stream);
 }
