@@ -95,10 +95,15 @@ __device__ __forceinline__ float finish_lse(float m, float total) {  // base 2 -
 // columns query rows, so that one decoded token with up to 8 heads per KV head
 // wastes nothing of a tile, and a thread's score columns are its output
 // columns.  The codes are the A operand straight from registers: a nibble
-// becomes a half by one logic operation (1024 + n or 64 + n) and one exact
-// subtraction.  The group scales stay out of the products: a key's scale
-// multiplies the finished dot product of its group, a value's scale its
-// weight, so each product is code * half, exact in fp32.
+// n = code + 8 becomes a half by one logic operation (1024 + n or 64 + n) and one
+// exact subtraction, nine operations for eight nibbles.  Five are enough for the
+// subnormals n 2^-24 and n 2^-20 that masked words are already, with the 8 taken
+// off the sums; but the tensor cores align a sum's terms by their exponent
+// fields, and a subnormal's leading zeros are bits the sum loses (errors of 2^-10
+// of a code step were seen).
+// The group scales stay out of the products: a key's scale multiplies the
+// finished dot product of its group, a value's scale its weight, so each product
+// is code * half, exact in fp32.
 //
 // Queries are scaled by a power of two per row to fit halves without loss
 // (elements 2^-24 below the row's largest lose bits that fp32 sums of the row
@@ -110,8 +115,7 @@ __device__ __forceinline__ float finish_lse(float m, float total) {  // base 2 -
 // The reference exponent moves only when a scaled weight would exceed 2^15 (one
 // vote per tile); the exact maximum is not needed, as l and O share it.
 constexpr int kAttnWarps = 4;
-constexpr int kStages = 4;
-constexpr int kLeastShare = 16;  // tiles: 4 for each warp
+constexpr int kLeastShare = 32;  // tiles: 8 for each warp
 constexpr float kOffset = 7.0f, kLargest = 32768.0f;
 
 template <int D>
@@ -120,6 +124,8 @@ struct Kv4Tile {  // bytes of one 16-token tile of one KV head
     static constexpr int kCodes = 16 * D / 2;
     static constexpr int kScales = 16 * kGroups * 2;
     static constexpr int kBytes = 2 * (kCodes + kScales);  // K codes, V codes, K scales, V scales
+    static constexpr int kStages = D == 256 ? 2 : 3;       // steps of two tiles in a warp's ring
+    static constexpr int kRing = kStages * 2 * kBytes;
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
@@ -133,7 +139,7 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint32_t nib(uint32_t w, uint32_t mask, uint32_t magic) {  // (w & mask) | magic
+__device__ __forceinline__ uint32_t mask_or(uint32_t w, uint32_t mask, uint32_t magic) {  // (w & mask) | magic
     uint32_t d;
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(mask), "r"(magic));
     return d;
@@ -143,13 +149,13 @@ __device__ __forceinline__ uint32_t sub_half2(uint32_t a, uint32_t b) {
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-// Nibbles i and i + 4 of w as halves (code), i = 0 .. 3.
+// Codes i and i + 4 of w as halves, i = 0 .. 3.
 __device__ __forceinline__ void codes8(uint32_t w, uint32_t (&h)[4]) {
     const uint32_t x = w >> 8;
-    h[0] = sub_half2(nib(w, 0x000F000Fu, 0x64006400u), 0x64086408u);  // 1024 + n - 1032
-    h[1] = sub_half2(nib(w, 0x00F000F0u, 0x54005400u), 0x54805480u);  // 64 + n - 72
-    h[2] = sub_half2(nib(x, 0x000F000Fu, 0x64006400u), 0x64086408u);
-    h[3] = sub_half2(nib(x, 0x00F000F0u, 0x54005400u), 0x54805480u);
+    h[0] = sub_half2(mask_or(w, 0x000F000Fu, 0x64006400u), 0x64086408u);  // 1024 + n - 1032
+    h[1] = sub_half2(mask_or(w, 0x00F000F0u, 0x54005400u), 0x54805480u);  // 64 + n - 72
+    h[2] = sub_half2(mask_or(x, 0x000F000Fu, 0x64006400u), 0x64086408u);
+    h[3] = sub_half2(mask_or(x, 0x00F000F0u, 0x54005400u), 0x54805480u);
 }
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -204,56 +210,65 @@ __device__ __forceinline__ void attend_unit(const Kv4AttnParams &p, const Seq &s
                                             int chunk_last, int slot) {
     using Tile = Kv4Tile<D>;
     constexpr int G = Tile::kGroups, R = 8 * NT;
+    constexpr int H = NT == 1 && D <= 128 ? 2 : 1;  // tiles whose products are formed together, as registers allow
     extern __shared__ __align__(128) char smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     const int rows = seq.rows * p.group;
     const int base_pos = seq.len - seq.rows;  // position of the sequence's row 0
 
-    char *mine = smem + warp * (kStages * Tile::kBytes);
+    constexpr int kStages = Tile::kStages, kStep = 2 * Tile::kBytes;
+    char *mine = smem + warp * Tile::kRing;
     const int32_t *table = p.block_table + b * p.table_stride;
 
-    // This lane's pieces of a tile: 16 bytes of codes for every 32 lanes,
-    // [group][token][half] in shared memory (V's tokens in the order 0, 2, .. 14,
-    // 1, 3, ..), and one 16-byte piece of scales.
+    // A step is two tiles; lanes 0 - 15 load the first, 16 - 31 the second.  A
+    // lane's pieces of a tile: 16 bytes of codes for every 16 lanes, kept as
+    // [group][token][half] (V's tokens in the order 0, 2, .. 14, 1, 3, .., so
+    // that both operands' reads are free of bank conflicts), and one 16-byte
+    // piece of scales.
     constexpr int kPieces = D / 32;  // of a token
-    const int token = lane / kPieces, part = lane % kPieces;
-    const uint32_t k_dst = smem_u32(mine) + (part / 2) * 512 + (part & 1) * 16 + token * 32;
-    const uint32_t v_dst = smem_u32(mine) + Tile::kCodes + (part / 2) * 512 + (part & 1) * 16 +
-                           (((token & 1) << 3) | (token >> 1)) * 32;
-    const int kv = lane / (Tile::kScales / 16);  // 0: K's scales, 1: V's, above: none
-    const uint32_t s_dst = smem_u32(mine) + 2 * Tile::kCodes + lane * 16;
-    const uint8_t *k_src = p.codes[0] + static_cast<int64_t>(kvh) * p.page_size * (D / 2) + lane * 16;
-    const uint8_t *v_src = p.codes[1] + static_cast<int64_t>(kvh) * p.page_size * (D / 2) + lane * 16;
-    const char *s_src = reinterpret_cast<const char *>(p.scales[kv & 1] + static_cast<int64_t>(kvh) * p.page_size * G) +
-                        (lane % (Tile::kScales / 16)) * 16;
+    const int half_warp = lane >> 4, sub = lane & 15;
+    const int token = sub / kPieces, part = sub % kPieces;
+    const uint32_t base_dst = smem_u32(mine) + half_warp * Tile::kBytes;
+    const uint32_t piece_dst = (part / 2) * 512 + (part & 1) * 16;
+    const int kv = sub / (Tile::kScales / 16);  // 0: K's scales, 1: V's, above: none
+    const int64_t head_cell = static_cast<int64_t>(kvh) * p.page_size;
+    const uint8_t *k_src = p.codes[0] + head_cell * (D / 2) + sub * 16;
+    const uint8_t *v_src = p.codes[1] + head_cell * (D / 2) + sub * 16;
+    const char *s_src = reinterpret_cast<const char *>(p.scales[kv & 1] + head_cell * G) + (sub % (Tile::kScales / 16)) * 16;
     const uint32_t page_codes = static_cast<uint32_t>(p.kv_heads) * p.page_size * (D / 2);
     const uint32_t page_scales = static_cast<uint32_t>(p.kv_heads) * p.page_size * (G * 2);
 
-    // The tile to load next: its number, its page's place in the table, its
-    // place in the page, and the page, read one step ahead of the copy.
+    // The tile this lane loads next: its number, its page's place in the table,
+    // its place in the page, and the page, read one step ahead of the copy.
+    constexpr int kAhead = 2 * kAttnWarps;
     const uint32_t page_tiles = static_cast<uint32_t>(p.page_size) / 16;
-    const uint32_t step_pages = kAttnWarps / page_tiles, step_rest = kAttnWarps % page_tiles;
-    int load_tile = chunk_first + warp;
+    const uint32_t step_pages = kAhead / page_tiles, step_rest = kAhead % page_tiles;
+    int load_tile = chunk_first + 2 * warp + half_warp;
     uint32_t load_page = static_cast<uint32_t>(load_tile) / page_tiles, load_off = static_cast<uint32_t>(load_tile) % page_tiles;
     int32_t page = load_tile < chunk_last ? __ldg(table + load_page) : -1;
-    uint32_t held = 0;  // bit 0: the tile at hand is there, bit i: the i-th after it
+    uint32_t held = 0;  // bits 0 and 1: the step's two tiles are there; the next steps' above
 
     auto issue = [&](int stage) {
         const bool there = page >= 0 && page < p.num_pages;
-        held = (held >> 1) | (there ? 1u << (kStages - 1) : 0u);
+        const uint32_t both = __ballot_sync(0xFFFFFFFFu, there);
+        held = (held >> 2) | ((both & 1u) | (both >> 16 & 1u) * 2u) << (2 * (kStages - 1));
         if (there) {
-            const uint32_t at = stage * Tile::kBytes;
+            const uint32_t at = base_dst + stage * kStep;
             const uint64_t codes = static_cast<uint64_t>(static_cast<uint32_t>(page)) * page_codes + load_off * Tile::kCodes;
             const uint64_t scales = static_cast<uint64_t>(static_cast<uint32_t>(page)) * page_scales + load_off * Tile::kScales;
+            const uint8_t *k = k_src + codes, *v = v_src + codes;
+            const uint32_t k_dst = at + piece_dst + token * 32;
+            const uint32_t v_dst = at + Tile::kCodes + piece_dst;
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                cp_async16(k_dst + at + i * (32 / kPieces) * 32, k_src + codes + i * 512);
-                cp_async16(v_dst + at + i * (16 / kPieces) * 32, v_src + codes + i * 512);
+            for (int i = 0; i < D / 32; ++i) {
+                const int t = token + i * (16 / kPieces);
+                cp_async16(k_dst + i * (16 / kPieces) * 32, k + i * 256);
+                cp_async16(v_dst + (((t & 1) << 3) | (t >> 1)) * 32, v + i * 256);
             }
-            if (kv < 2) cp_async16(s_dst + at, s_src + scales);
+            if (kv < 2) cp_async16(at + 2 * Tile::kCodes + sub * 16, s_src + scales);
         }
         cp_commit();
-        load_tile += kAttnWarps;
+        load_tile += kAhead;
         load_page += step_pages;
         load_off += step_rest;
         if (load_off >= page_tiles) load_off -= page_tiles, ++load_page;
@@ -306,10 +321,10 @@ __device__ __forceinline__ void attend_unit(const Kv4AttnParams &p, const Seq &s
         amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
         int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
-        ex = amax == 0.0f ? 10 : max(ex, -100);
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + 10 - ex) << 23);  // 2^(10 - ex)
+        ex = amax == 0.0f ? 14 : max(ex, -100);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - ex) << 23);  // 2^(14 - ex)
         // back, times the caller's scale and log2(e)
-        const float mul = p.scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 - 10 + ex) << 23);
+        const float mul = p.scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 - 14 + ex) << 23);
 #pragma unroll
         for (int gr = 0; gr < G; ++gr)
 #pragma unroll
@@ -337,99 +352,130 @@ __device__ __forceinline__ void attend_unit(const Kv4AttnParams &p, const Seq &s
             l[j][e] = 0.0f;
         }
     bool unset = true;  // some row has no reference yet
-
     int stage = 0;
-    for (int tile = chunk_first + warp; tile < chunk_last; tile += kAttnWarps) {
+#pragma unroll 1
+    for (int tile = chunk_first + 2 * warp; tile < chunk_last; tile += kAhead) {
         issue(stage == 0 ? kStages - 1 : stage - 1);
         cp_wait<kStages - 1>();
         __syncwarp();
-        if (held & 1u) {
-            const char *kc = mine + stage * Tile::kBytes, *vc = kc + Tile::kCodes;
-            const __half *ks = reinterpret_cast<const __half *>(kc + 2 * Tile::kCodes);
-            const __half *vs = ks + 16 * G;
-            float s[NT][4];
+        const char *step = mine + stage * kStep;
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+        if ((held & 3u) == 0) continue;
+#pragma unroll 1
+        for (int part = 0; part < 2 / H; ++part) {
+            const char *at = step + part * Tile::kBytes;
+            const int t0 = (tile + part) * 16;
+            const uint32_t there = held >> part & (H == 2 ? 3u : 1u);
+            float s[H][NT][4];
 #pragma unroll
-            for (int gr = 0; gr < G; ++gr) {
-                const uint2 ka = *reinterpret_cast<const uint2 *>(kc + gr * 512 + g * 32 + c * 8);
-                const uint2 kb = *reinterpret_cast<const uint2 *>(kc + gr * 512 + (g + 8) * 32 + c * 8);
-                const float sa = __half2float(ks[g * G + gr]), sb = __half2float(ks[(g + 8) * G + gr]);
-                uint32_t a[2][4], bq[2][4];
-                codes8(ka.x, a[0]);
-                codes8(ka.y, a[1]);
-                codes8(kb.x, bq[0]);
-                codes8(kb.y, bq[1]);
+            for (int h = 0; h < H; ++h) {
+                const char *kc = at + h * Tile::kBytes;
+                const __half *ks = reinterpret_cast<const __half *>(kc + 2 * Tile::kCodes);
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    float acc[4];
-                    mma16816_first(acc, a[0][0], bq[0][0], a[0][1], bq[0][1], q[j][gr][0], q[j][gr][1]);
+                for (int gr = 0; gr < G; ++gr) {
+                    const uint2 ka = *reinterpret_cast<const uint2 *>(kc + gr * 512 + g * 32 + c * 8);
+                    const uint2 kb = *reinterpret_cast<const uint2 *>(kc + gr * 512 + (g + 8) * 32 + c * 8);
+                    const float sa = __half2float(ks[g * G + gr]), sb = __half2float(ks[(g + 8) * G + gr]);
+                    uint32_t a[2][4], bq[2][4];
+                    codes8(ka.x, a[0]);
+                    codes8(ka.y, a[1]);
+                    codes8(kb.x, bq[0]);
+                    codes8(kb.y, bq[1]);
 #pragma unroll
-                    for (int w = 0; w < 2; ++w)
+                    for (int j = 0; j < NT; ++j) {
+                        float acc[4];
+                        mma16816_first(acc, a[0][0], bq[0][0], a[0][1], bq[0][1], q[j][gr][0], q[j][gr][1]);
 #pragma unroll
-                        for (int i = w == 0 ? 2 : 0; i < 4; i += 2)
-                            mma16816(acc, a[w][i], bq[w][i], a[w][i + 1], bq[w][i + 1], q[j][gr][4 * w + i],
-                                     q[j][gr][4 * w + i + 1]);
-                    s[j][0] = gr == 0 ? acc[0] * sa : fmaf(acc[0], sa, s[j][0]);
-                    s[j][1] = gr == 0 ? acc[1] * sa : fmaf(acc[1], sa, s[j][1]);
-                    s[j][2] = gr == 0 ? acc[2] * sb : fmaf(acc[2], sb, s[j][2]);
-                    s[j][3] = gr == 0 ? acc[3] * sb : fmaf(acc[3], sb, s[j][3]);
+                        for (int w = 0; w < 2; ++w)
+#pragma unroll
+                            for (int i = w == 0 ? 2 : 0; i < 4; i += 2)
+                                mma16816(acc, a[w][i], bq[w][i], a[w][i + 1], bq[w][i + 1], q[j][gr][4 * w + i],
+                                         q[j][gr][4 * w + i + 1]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            s[h][j][e] = gr == 0 ? acc[e] * (e < 2 ? sa : sb) : fmaf(acc[e], e < 2 ? sa : sb, s[h][j][e]);
+                    }
                 }
             }
-            float vscale[G][2];
+            float vscale[H][G][2];
 #pragma unroll
-            for (int gr = 0; gr < G; ++gr) {
-                vscale[gr][0] = __half2float(vs[g * G + gr]);
-                vscale[gr][1] = __half2float(vs[(g + 8) * G + gr]);
+            for (int h = 0; h < H; ++h) {
+                const __half *vs = reinterpret_cast<const __half *>(at + h * Tile::kBytes + 2 * Tile::kCodes + Tile::kScales);
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr) {
+                    vscale[h][gr][0] = __half2float(vs[g * G + gr]);
+                    vscale[h][gr][1] = __half2float(vs[(g + 8) * G + gr]);
+                }
             }
-            const int t0 = tile * 16;
-            const bool masked = t0 + 15 > lowest || (p.window > 0 && t0 <= highest - p.window);
-            float w[NT][4], x[NT][G][4];
-            auto weigh = [&](int j, int e, bool hide) {
-                w[j][e] = hide ? 0.0f : ex2(fmaf(s[j][e], qmul[j][e & 1], ref[j][e & 1]));
+            // weights: packed products with the value scales, and what l grows by
+            uint32_t pk[H][NT][G][2];
+            float grown[H][NT][2];
+            float big = 0.0f;
+            auto weigh = [&](int h, int j, uint32_t hide) {
+                float w[4];
 #pragma unroll
-                for (int gr = 0; gr < G; ++gr)  // a hidden token's scale may be anything
-                    x[j][gr][e] = hide ? 0.0f : w[j][e] * vscale[gr][e >> 1];
+                for (int e = 0; e < 4; ++e)
+                    w[e] = hide >> e & 1u ? 0.0f : ex2(fmaf(s[h][j][e], qmul[j][e & 1], ref[j][e & 1]));
+                grown[h][j][0] = w[0] + w[2];
+                grown[h][j][1] = w[1] + w[3];
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr) {
+                    float x[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {  // a hidden token's scale may be anything
+                        x[e] = hide >> e & 1u ? 0.0f : w[e] * vscale[h][gr][e >> 1];
+                        big = fmaxf(big, x[e]);
+                    }
+                    pk[h][j][gr][0] = pack_half2(x[0], x[1]);
+                    pk[h][j][gr][1] = pack_half2(x[2], x[3]);
+                }
             };
-            uint32_t hidden = 0;  // bit 4 j + e: weight e of query tile j
+            const bool masked =
+                there != (H == 2 ? 3u : 1u) || t0 + 16 * H - 1 > lowest || (p.window > 0 && t0 <= highest - p.window);
+            uint32_t hidden = 0;  // bit 4 (NT h + j) + e
             if (masked) {
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+                for (int h = 0; h < H; ++h)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int t = t0 + g + (e & 2) * 4, pos = top[j][e & 1];
-                        const bool hide = t > pos || (p.window > 0 && t <= pos - p.window);
-                        hidden |= hide ? 1u << (4 * j + e) : 0u;
-                        weigh(j, e, hide);
+                    for (int j = 0; j < NT; ++j) {
+                        uint32_t hide = 0;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int t = t0 + 16 * h + g + (e & 2) * 4, pos = top[j][e & 1];
+                            if (t > pos || (p.window > 0 && t <= pos - p.window) || !(there >> h & 1u)) hide |= 1u << e;
+                        }
+                        weigh(h, j, hide);
+                        hidden |= hide << (4 * (NT * h + j));
                     }
             } else {
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+                for (int h = 0; h < H; ++h)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) weigh(j, e, false);
+                    for (int j = 0; j < NT; ++j) weigh(h, j, 0u);
             }
-            float big = 0.0f;
+            if (unset || __any_sync(0xFFFFFFFFu, big > kLargest)) {
+                float lv[H][2];  // log2 of each token's largest value scale, kept to what halves can hold
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+                for (int h = 0; h < H; ++h)
 #pragma unroll
-                for (int gr = 0; gr < G; ++gr)
+                    for (int t = 0; t < 2; ++t) {
+                        float v = vscale[h][0][t];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) big = fmaxf(big, x[j][gr][e]);
-            const bool over = big > kLargest;
-            if (unset || __any_sync(0xFFFFFFFFu, over)) {
-                float lv[2];  // log2 of each token's largest value scale, kept to what halves can hold
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    float v = vscale[0][t];
-#pragma unroll
-                    for (int gr = 1; gr < G; ++gr) v = fmaxf(v, vscale[gr][t]);
-                    lv[t] = fminf(fmaxf(lg2(v), -24.0f), 16.0f);
-                }
+                        for (int gr = 1; gr < G; ++gr) v = fmaxf(v, vscale[h][gr][t]);
+                        lv[h][t] = fminf(fmaxf(lg2(v), -24.0f), 16.0f);
+                    }
                 bool none = false;
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float y = hidden >> (4 * j + e) & 1u ? -INFINITY : fmaf(s[j][e], qmul[j][e], lv[0]);
-                        y = fmaxf(y, hidden >> (4 * j + e + 2) & 1u ? -INFINITY : fmaf(s[j][e + 2], qmul[j][e], lv[1]));
+                        float y = -INFINITY;
+#pragma unroll
+                        for (int h = 0; h < H; ++h)
+#pragma unroll
+                            for (int t = 0; t < 2; ++t)
+                                if (!(hidden >> (4 * (NT * h + j) + 2 * t + e) & 1u))
+                                    y = fmaxf(y, fmaf(s[h][j][2 * t + e], qmul[j][e], lv[h][t]));
                         y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 4));
                         y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 8));
                         y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 16));
@@ -446,45 +492,47 @@ __device__ __forceinline__ void attend_unit(const Kv4AttnParams &p, const Seq &s
                     }
                 unset = __any_sync(0xFFFFFFFFu, none);
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+                for (int h = 0; h < H; ++h)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) weigh(j, e, hidden >> (4 * j + e) & 1u);
+                    for (int j = 0; j < NT; ++j) weigh(h, j, hidden >> (4 * (NT * h + j)));
             }
-            uint32_t pb[NT][G][2];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                l[j][0] += w[j][0] + w[j][2];
-                l[j][1] += w[j][1] + w[j][3];
+            for (int h = 0; h < H; ++h) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    l[j][0] += grown[h][j][0];
+                    l[j][1] += grown[h][j][1];
+#pragma unroll
+                    for (int gr = 0; gr < G; ++gr) {
+                        pk[h][j][gr][0] = transpose8x8(pk[h][j][gr][0]);
+                        pk[h][j][gr][1] = transpose8x8(pk[h][j][gr][1]);
+                    }
+                }
+                const char *vc = at + h * Tile::kBytes + Tile::kCodes;
 #pragma unroll
                 for (int gr = 0; gr < G; ++gr) {
-                    pb[j][gr][0] = transpose8x8(pack_half2(x[j][gr][0], x[j][gr][1]));
-                    pb[j][gr][1] = transpose8x8(pack_half2(x[j][gr][2], x[j][gr][3]));
-                }
-            }
+                    const char *vg = vc + gr * 512 + g * 4;
+                    const uint32_t w0 = *reinterpret_cast<const uint32_t *>(vg + c * 32);         // token 2c
+                    const uint32_t w1 = *reinterpret_cast<const uint32_t *>(vg + (8 + c) * 32);   // 2c + 1
+                    const uint32_t w2 = *reinterpret_cast<const uint32_t *>(vg + (4 + c) * 32);   // 2c + 8
+                    const uint32_t w3 = *reinterpret_cast<const uint32_t *>(vg + (12 + c) * 32);  // 2c + 9
 #pragma unroll
-            for (int gr = 0; gr < G; ++gr) {
-                const char *vg = vc + gr * 512 + g * 4;
-                const uint32_t w0 = *reinterpret_cast<const uint32_t *>(vg + c * 32);          // token 2c
-                const uint32_t w1 = *reinterpret_cast<const uint32_t *>(vg + (8 + c) * 32);    // 2c + 1
-                const uint32_t w2 = *reinterpret_cast<const uint32_t *>(vg + (4 + c) * 32);    // 2c + 8
-                const uint32_t w3 = *reinterpret_cast<const uint32_t *>(vg + (12 + c) * 32);   // 2c + 9
+                    for (int d = 0; d < 2; ++d) {  // dims 8g + 4d .. + 3: pairs of tokens
+                        const uint32_t sel = d ? 0x7632u : 0x5410u;
+                        uint32_t a[4], bq[4];
+                        codes8(__byte_perm(w0, w1, sel), a);
+                        codes8(__byte_perm(w2, w3, sel), bq);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {  // dims 8g + 4h .. + 3: pairs of tokens
-                    const uint32_t sel = h ? 0x7632u : 0x5410u;
-                    uint32_t a[4], bq[4];
-                    codes8(__byte_perm(w0, w1, sel), a);
-                    codes8(__byte_perm(w2, w3, sel), bq);
+                        for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int j = 0; j < NT; ++j)
-                            mma16816(o[j][gr * 4 + h * 2 + i], a[2 * i], a[2 * i + 1], bq[2 * i], bq[2 * i + 1],
-                                     pb[j][gr][0], pb[j][gr][1]);
+                            for (int j = 0; j < NT; ++j)
+                                mma16816(o[j][gr * 4 + d * 2 + i], a[2 * i], a[2 * i + 1], bq[2 * i], bq[2 * i + 1],
+                                         pk[h][j][gr][0], pk[h][j][gr][1]);
+                    }
                 }
             }
         }
         __syncwarp();
-        stage = stage + 1 == kStages ? 0 : stage + 1;
     }
     cp_wait<0>();
     __syncwarp();
@@ -510,7 +558,7 @@ __device__ __forceinline__ void attend_unit(const Kv4AttnParams &p, const Seq &s
             }
         }
     __syncthreads();
-    constexpr int kStride = kStages * Tile::kBytes / 4;
+    constexpr int kStride = Tile::kRing / 4;
     const float *all = reinterpret_cast<const float *>(smem);
     for (int i = threadIdx.x; i < R * (D / 4); i += kAttnWarps * 32) {
         const int r = i / (D / 4), d = (i % (D / 4)) * 4;
@@ -603,7 +651,7 @@ __device__ __forceinline__ Share find_share(const Kv4AttnParams &p, int tile_row
 
 // CTAs resident on an SM: what 64 K registers hold.
 template <int D, int NT>
-constexpr int kResident = D == 64 ? (NT == 1 ? 6 : 4) : D == 128 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 3 : 2);
+constexpr int kResident = D == 64 ? (NT == 1 ? 6 : 4) : D == 128 ? (NT == 1 ? 4 : 3) : 2;
 
 template <typename E, int D, int NT>
 __global__ void __launch_bounds__(kAttnWarps * 32, kResident<D, NT>) kv4_attention_kernel(const __grid_constant__ Kv4AttnParams p) {
@@ -715,12 +763,12 @@ constexpr int kSms = 148;
 Plan plan(int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t max_q_len, int32_t max_seq_len) {
     Plan pl{};
     const int64_t rows = (int64_t)max_q_len * (q_heads / kv_heads);
-    pl.n_tiles = rows <= 8 ? 1 : 2;
+    pl.n_tiles = rows <= 8 || head_dim == 256 ? 1 : 2;  // 16 rows of 256 dims do not fit the registers
     pl.row_tiles = (int32_t)((rows + 8 * pl.n_tiles - 1) / (8 * pl.n_tiles));
     pl.pairs = (int64_t)B * pl.row_tiles;
     const int64_t units = pl.pairs * kv_heads, tiles = ((int64_t)max_seq_len + 15) / 16;
     const int resident = pl.n_tiles == 1 ? (head_dim == 64 ? kResident<64, 1> : head_dim == 128 ? kResident<128, 1> : kResident<256, 1>)
-                                         : (head_dim == 64 ? kResident<64, 2> : head_dim == 128 ? kResident<128, 2> : kResident<256, 2>);
+                                         : (head_dim == 64 ? kResident<64, 2> : head_dim == 128 ? kResident<128, 2> : 2);
     const int64_t slots = (int64_t)kSms * resident;
     if (units >= 4 * slots || tiles <= 2 * kLeastShare) return pl;
     const int64_t most = (units * tiles + kLeastShare - 1) / kLeastShare;
@@ -730,8 +778,8 @@ Plan plan(int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_
 
 template <typename E, int D, int NT>
 qkn_status launch_attention(const Kv4AttnParams &p, dim3 grid, dim3 join_grid, void *stream) {
-    constexpr size_t smem = (size_t)kAttnWarps * kStages * Kv4Tile<D>::kBytes;
-    static_assert((size_t)8 * NT * (D + 2) * 4 <= kStages * Kv4Tile<D>::kBytes, "a warp's partial result must fit its ring");
+    constexpr size_t smem = (size_t)kAttnWarps * Kv4Tile<D>::kRing;
+    static_assert((size_t)8 * NT * (D + 2) * 4 <= Kv4Tile<D>::kRing, "a warp's partial result must fit its ring");
     const void *fn = (const void *)kv4_attention_kernel<E, D, NT>;
     if (smem > 48 * 1024) {
         cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -747,9 +795,8 @@ qkn_status launch_attention(const Kv4AttnParams &p, int d, dim3 grid, dim3 join_
         return d == 64    ? launch_attention<E, 64, 1>(p, grid, join_grid, stream)
                : d == 128 ? launch_attention<E, 128, 1>(p, grid, join_grid, stream)
                           : launch_attention<E, 256, 1>(p, grid, join_grid, stream);
-    return d == 64    ? launch_attention<E, 64, 2>(p, grid, join_grid, stream)
-           : d == 128 ? launch_attention<E, 128, 2>(p, grid, join_grid, stream)
-                      : launch_attention<E, 256, 2>(p, grid, join_grid, stream);
+    return d == 64 ? launch_attention<E, 64, 2>(p, grid, join_grid, stream)
+                   : launch_attention<E, 128, 2>(p, grid, join_grid, stream);
 }
 
 }  // namespace
