@@ -38,7 +38,7 @@ struct Kv4AttnParams {
     int32_t shared;                // whether units are cut at the CTAs' shares (else one CTA per unit)
     float *part_o;                 // shared: [grid][2][rows of a tile][head_dim], partial outputs
     float2 *part_s;                // and their (exponent, sum) pairs
-    int64_t *starts;               // [B * row_tiles] first tile of each sequence and query tile, then the share
+    int32_t *starts;               // [B * row_tiles] first tile of each sequence and query tile, then the share
 };
 
 // Rows and cached tokens of sequence b, kept inside the buffers.
@@ -60,6 +60,12 @@ __device__ __forceinline__ Seq sequence(const Kv4AttnParams &p, int b) {
     if (len > held) len = held;
     s.len = len < 0 ? 0 : static_cast<int32_t>(len);
     return s;
+}
+
+// a / b for 0 <= a < 2^21, b > 0: (a + 1/2) / b lies at least 1 / (2b) from the
+// integers, further than the reciprocal's error can move it.
+__device__ __forceinline__ int small_div(int a, int b) {
+    return static_cast<int>((static_cast<float>(a) + 0.5f) * __frcp_rn(static_cast<float>(b)));
 }
 
 // Four elements of the output, sum / total (zeros for a row without tokens).
@@ -198,7 +204,7 @@ struct TileRange {
 __device__ __forceinline__ TileRange tile_range(const Kv4AttnParams &p, const Seq &s, int r0, int n) {
     const int rows = s.rows * p.group;
     const int r1 = (r0 + n < rows ? r0 + n : rows) - 1;
-    const int lo = s.len - s.rows + r0 / p.group, hi = s.len - s.rows + r1 / p.group;  // positions
+    const int lo = s.len - s.rows + small_div(r0, p.group), hi = s.len - s.rows + small_div(r1, p.group);  // positions
     TileRange t{0, hi < 0 ? 0 : hi / 16 + 1};
     if (p.window > 0 && lo - p.window + 1 > 0) t.first = (lo - p.window + 1) / 16;
     if (t.first > t.last) t.first = t.last;
@@ -245,8 +251,37 @@ __device__ __forceinline__ void attend_unit(const Kv4AttnParams &p, const Seq &s
     const uint32_t step_pages = kAhead / page_tiles, step_rest = kAhead % page_tiles;
     int load_tile = chunk_first + 2 * warp + half_warp;
     uint32_t load_page = static_cast<uint32_t>(load_tile) / page_tiles, load_off = static_cast<uint32_t>(load_tile) % page_tiles;
-    int32_t page = load_tile < chunk_last ? __ldg(table + load_page) : -1;
+    int32_t page = -1, pages[kStages];
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) {  // the first steps' pages, all at once
+        uint32_t at = load_page + i * step_pages, off = load_off + i * step_rest;
+        while (off >= page_tiles) off -= page_tiles, ++at;
+        pages[i] = load_tile + i * kAhead < chunk_last ? __ldg(table + at) : -1;
+    }
     uint32_t held = 0;  // bits 0 and 1: the step's two tiles are there; the next steps' above
+
+    // This thread's part of query row 8 j + g: dims 64 gr + 16 c .. + 15.
+    uint4 raw[NT][G][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int r = r0 + 8 * j + g, i = small_div(r, p.group);
+        const int64_t row = seq.row0 + i;
+        const int head = kvh * p.group + r - i * p.group;
+        const char *src = p.q + row * p.q_stride + (static_cast<int64_t>(head) * D + 16 * c) * sizeof(E);
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                raw[j][gr][h] = make_uint4(0, 0, 0, 0);
+                if (r >= rows) continue;
+                if (p.q_vector) {
+                    raw[j][gr][h] = *reinterpret_cast<const uint4 *>(src + gr * 128 + h * 16);
+                } else {
+                    const uint16_t *u = reinterpret_cast<const uint16_t *>(src + gr * 128 + h * 16);
+                    raw[j][gr][h] = make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
+                }
+            }
+    }
 
     auto issue = [&](int stage) {
         const bool there = page >= 0 && page < p.num_pages;
@@ -272,48 +307,33 @@ __device__ __forceinline__ void attend_unit(const Kv4AttnParams &p, const Seq &s
         load_page += step_pages;
         load_off += step_rest;
         if (load_off >= page_tiles) load_off -= page_tiles, ++load_page;
-        page = load_tile < chunk_last ? __ldg(table + load_page) : -1;
     };
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(i);
+    for (int i = 0; i < kStages - 1; ++i) {
+        page = pages[i];
+        issue(i);
+    }
+    page = pages[kStages - 1];
 
-    // Queries: this thread's B operands (row 8 j + g, dims 64 gr + 16 c .. + 15)
-    // and, for its score columns 2c and 2c + 1, the row's factor and limits.
+    // Queries: this thread's B operands and, for its score columns 2c and 2c + 1, the row's factor and limits.
     uint32_t q[NT][G][8];
     float qmul[NT][2];
     int top[NT][2];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-        const int r = r0 + 8 * j + g;
         float x[G][16];
         float amax = 0.0f;
-        const int64_t row = seq.row0 + r / p.group;
-        const int head = kvh * p.group + r % p.group;
-        const char *src = p.q + row * p.q_stride + (static_cast<int64_t>(head) * D + 16 * c) * sizeof(E);
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
-            if (p.q_vector) {
-                uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-                if (r < rows) {
-                    v[0] = *reinterpret_cast<const uint4 *>(src + gr * 128);
-                    v[1] = *reinterpret_cast<const uint4 *>(src + gr * 128 + 16);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                F2 w[4];
+                Elem<E>::widen(raw[j][gr][h], w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[gr][8 * h + 2 * e] = f2_lo(w[e]);
+                    x[gr][8 * h + 2 * e + 1] = f2_hi(w[e]);
                 }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    F2 w[4];
-                    Elem<E>::widen(v[h], w);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[gr][8 * h + 2 * e] = f2_lo(w[e]);
-                        x[gr][8 * h + 2 * e + 1] = f2_hi(w[e]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    x[gr][e] = r < rows ? Elem<E>::to_float(
-                                              reinterpret_cast<const typename Elem<E>::Bits *>(src + gr * 128)[e])
-                                        : 0.0f;
             }
 #pragma unroll
             for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[gr][e]));
@@ -335,11 +355,11 @@ __device__ __forceinline__ void attend_unit(const Kv4AttnParams &p, const Seq &s
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             qmul[j][e] = __shfl_sync(0xFFFFFFFFu, mul, (2 * c + e) * 4);
-            top[j][e] = base_pos + (r0 + 8 * j + 2 * c + e) / p.group;
+            top[j][e] = base_pos + small_div(r0 + 8 * j + 2 * c + e, p.group);
         }
     }
-    const int lowest = base_pos + r0 / p.group;                                    // the tile's first row
-    const int highest = base_pos + (min(r0 + R, rows) - 1) / p.group;
+    const int lowest = base_pos + small_div(r0, p.group);                                    // the tile's first row
+    const int highest = base_pos + small_div(min(r0 + R, rows) - 1, p.group);
 
     // ref: kOffset - the rows' reference exponents (infinity: none yet; rows that see nothing need none)
     float o[NT][D / 16][4] = {};
@@ -356,6 +376,7 @@ __device__ __forceinline__ void attend_unit(const Kv4AttnParams &p, const Seq &s
 #pragma unroll 1
     for (int tile = chunk_first + 2 * warp; tile < chunk_last; tile += kAhead) {
         issue(stage == 0 ? kStages - 1 : stage - 1);
+        page = load_tile < chunk_last ? __ldg(table + load_page) : -1;
         cp_wait<kStages - 1>();
         __syncwarp();
         const char *step = mine + stage * kStep;
@@ -580,8 +601,9 @@ __device__ __forceinline__ void attend_unit(const Kv4AttnParams &p, const Seq &s
             sum.w = fmaf(v.w, f, sum.w);
             total = fmaf(pw[R * D + R + r], f, total);
         }
-        const int64_t row = seq.row0 + (r0 + r) / p.group;
-        const int head = kvh * p.group + (r0 + r) % p.group;
+        const int qi = small_div(r0 + r, p.group);
+        const int64_t row = seq.row0 + qi;
+        const int head = kvh * p.group + r0 + r - qi * p.group;
         if (slot >= 0) {
             const int64_t cell = static_cast<int64_t>(slot) * R + r;
             *reinterpret_cast<float4 *>(p.part_o + cell * D + d) = sum;
@@ -593,52 +615,53 @@ __device__ __forceinline__ void attend_unit(const Kv4AttnParams &p, const Seq &s
     }
 }
 
-// Tiles of sequence b's query tile rt: at least one for rows that exist (a row
-// without tokens is still answered), times the KV heads.
-__device__ __forceinline__ int64_t pair_tiles(const Kv4AttnParams &p, int b, int rt, int tile_rows) {
+// Tiles of a (sequence, query tile) pair: at least one for rows that exist (a
+// row without tokens is still answered), times the KV heads.  All units' tiles
+// are fewer than 2^31 (the host sees to it).
+__device__ __forceinline__ int pair_tiles(const Kv4AttnParams &p, int pair, int tile_rows) {
+    const int b = p.row_tiles == 1 ? pair : pair / p.row_tiles, r0 = (pair - b * p.row_tiles) * tile_rows;
     const Seq s = sequence(p, b);
-    if (rt * tile_rows >= s.rows * p.group) return 0;
-    const TileRange t = tile_range(p, s, rt * tile_rows, tile_rows);
-    return static_cast<int64_t>(max(t.last - t.first, 1)) * p.kv_heads;
+    if (r0 >= s.rows * p.group) return 0;
+    const TileRange t = tile_range(p, s, r0, tile_rows);
+    return max(t.last - t.first, 1) * p.kv_heads;
 }
 
-// This CTA's share of all units' tiles: [first, last), and the (sequence, query
-// tile) pair it begins in, `at` tiles into it.
+// This CTA's share of all units' tiles: how many, and the pair it begins in,
+// `at` tiles into it.
 struct Share {
-    int64_t tiles, at;
-    int pair;
+    int tiles, at, pair;
 };
 __device__ __forceinline__ Share find_share(const Kv4AttnParams &p, int tile_rows) {
-    __shared__ int64_t sums[kAttnWarps];
+    __shared__ int sums[kAttnWarps];
     __shared__ Share found;
     const int n = p.B * p.row_tiles, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int slice = (n + kAttnWarps * 32 - 1) / (kAttnWarps * 32);
     const int i0 = min(static_cast<int>(threadIdx.x) * slice, n), i1 = min(i0 + slice, n);
-    int64_t sum = 0;
-    for (int i = i0; i < i1; ++i) sum += pair_tiles(p, i / p.row_tiles, i % p.row_tiles, tile_rows);
-    int64_t before = sum;
+    int sum = 0;
+    for (int i = i0; i < i1; ++i) sum += pair_tiles(p, i, tile_rows);
+    int before = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, before, off);
+        const int v = __shfl_up_sync(0xFFFFFFFFu, before, off);
         if (lane >= off) before += v;
     }
     if (lane == 31) sums[warp] = before;
+    if (threadIdx.x == 0) found = Share{0, 0, 0};
     __syncthreads();
-    int64_t total = 0;
+    int total = 0;
     before -= sum;
+#pragma unroll
     for (int w = 0; w < kAttnWarps; ++w) {
         if (w < warp) before += sums[w];
         total += sums[w];
     }
-    const int64_t share = max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kLeastShare));
-    const int64_t first = share * blockIdx.x;
-    if (threadIdx.x == 0) found = Share{0, 0, 0};
-    __syncthreads();
-    const bool mine = first >= before && first < before + sum;
-    if (blockIdx.x == 0 || mine) {
-        int64_t at = before;
+    const int share = max(static_cast<int>((static_cast<unsigned>(total) + gridDim.x - 1) / gridDim.x), kLeastShare);
+    const int64_t start = static_cast<int64_t>(share) * blockIdx.x;
+    const int first = start < total ? static_cast<int>(start) : total;
+    if (blockIdx.x == 0 || (first >= before && first < before + sum)) {
+        int at = before;
         for (int i = i0; i < i1; ++i) {
-            const int64_t c = pair_tiles(p, i / p.row_tiles, i % p.row_tiles, tile_rows);
+            const int c = slice == 1 ? sum : pair_tiles(p, i, tile_rows);
             if (blockIdx.x == 0) p.starts[i] = at;
             if (first >= at && first < at + c) found = Share{min(share, total - first), first - at, i};
             at += c;
@@ -651,7 +674,7 @@ __device__ __forceinline__ Share find_share(const Kv4AttnParams &p, int tile_row
 
 // CTAs resident on an SM: what 64 K registers hold.
 template <int D, int NT>
-constexpr int kResident = D == 64 ? (NT == 1 ? 6 : 4) : D == 128 ? (NT == 1 ? 4 : 3) : 2;
+constexpr int kResident = D == 64 ? (NT == 1 ? 5 : 4) : D == 128 ? 3 : 2;
 
 template <typename E, int D, int NT>
 __global__ void __launch_bounds__(kAttnWarps * 32, kResident<D, NT>) kv4_attention_kernel(const __grid_constant__ Kv4AttnParams p) {
@@ -673,9 +696,9 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kResident<D, NT>) kv4_attenti
         if (r0 >= seq.rows * p.group) continue;
         const TileRange range = tile_range(p, seq, r0, R);
         const int count = max(range.last - range.first, 1);
-        for (int kvh = static_cast<int>(mine.at / count); kvh < p.kv_heads && mine.tiles > 0; ++kvh) {
-            const int skip = static_cast<int>(mine.at - static_cast<int64_t>(kvh) * count);
-            const int take = static_cast<int>(min(static_cast<int64_t>(count - skip), mine.tiles));
+        for (int kvh = mine.at / count; kvh < p.kv_heads && mine.tiles > 0; ++kvh) {
+            const int skip = mine.at - kvh * count;
+            const int take = min(count - skip, mine.tiles);
             // a CTA has at most one unit that it only ends (or passes through) and one that it only begins
             const int slot = take == count ? -1 : static_cast<int>(blockIdx.x) * 2 + (skip == 0 ? 1 : 0);
             attend_unit<E, D, NT>(p, seq, b, kvh, r0, range.first + skip, min(range.first + skip + take, range.last), slot);
@@ -689,11 +712,11 @@ __global__ void __launch_bounds__(kAttnWarps * 32, kResident<D, NT>) kv4_attenti
 
 // Joins the units that the shares cut: one CTA per unit and row, its warps
 // taking the partial results in turn.
-constexpr int kJoinWarps = 4;
+constexpr int kJoinWarps = 8;
 template <typename E, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const __grid_constant__ Kv4AttnParams p) {
     pdl_wait_and_release();
-    __shared__ float held[kJoinWarps][D + 1];
+    __shared__ float held[kJoinWarps][D + 2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int pair = static_cast<int>(blockIdx.x) / p.kv_heads, kvh = static_cast<int>(blockIdx.x) % p.kv_heads;
     const int tile_rows = 8 * p.n_tiles, r0 = pair % p.row_tiles * tile_rows;
@@ -702,46 +725,61 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv4_join_kernel(const __grid_
     if (r >= seq.rows * p.group) return;
     const TileRange range = tile_range(p, seq, r0, tile_rows);
     const int count = max(range.last - range.first, 1);
-    const int64_t share = p.starts[p.B * p.row_tiles], start = p.starts[pair] + static_cast<int64_t>(kvh) * count;
-    const int64_t cta0 = start / share;
-    const int n = static_cast<int>((start + count - 1) / share - cta0) + 1;
+    const int share = p.starts[p.B * p.row_tiles], start = p.starts[pair] + kvh * count;
+    const int cta0 = start / share;
+    const int n = (start + count - 1) / share - cta0 + 1;
     if (n == 1) return;
     const int64_t row = seq.row0 + r / p.group;
     const int head = kvh * p.group + r % p.group;
     // partial k: the first CTA's begun unit, then the later ones' ended (or passed) unit
-    auto cell_of = [&](int k) -> int64_t { return ((cta0 + k) * 2 + (k == 0 ? 1 : 0)) * tile_rows + blockIdx.y; };
-    float top_m = -INFINITY;
-    for (int k = lane; k < n; k += 32) top_m = fmaxf(top_m, p.part_s[cell_of(k)].x);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top_m = fmaxf(top_m, __shfl_xor_sync(0xFFFFFFFFu, top_m, off));
+    auto cell_of = [&](int k) -> int64_t { return static_cast<int64_t>((cta0 + k) * 2 + (k == 0 ? 1 : 0)) * tile_rows + blockIdx.y; };
+    // each warp joins its share against its own largest exponent, read by lane
     constexpr int N = D / 32;
     float sum[N] = {};
-    float total = 0.0f;
-#pragma unroll 4
-    for (int k = warp; k < n; k += kJoinWarps) {
-        const int64_t cell = cell_of(k);
-        const float2 st = p.part_s[cell];
-        const float f = st.x == -INFINITY ? 0.0f : ex2(st.x - top_m);
-        total = fmaf(st.y, f, total);
-        const float *o = p.part_o + cell * D + lane;
+    float total = 0.0f, most = -INFINITY;
+    for (int k0 = 0; warp + k0 * kJoinWarps < n; k0 += 32) {
+        const int mine = warp + (k0 + lane) * kJoinWarps, here = min(32, (n - warp + kJoinWarps - 1) / kJoinWarps - k0);
+        const float2 st = lane < here ? p.part_s[cell_of(mine)] : make_float2(-INFINITY, 0.0f);
+        float m = fmaxf(most, st.x);
 #pragma unroll
-        for (int e = 0; e < N; ++e) sum[e] = fmaf(o[32 * e], f, sum[e]);
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+        const float back = most == -INFINITY ? 0.0f : ex2(most - m);
+        total *= back;
+#pragma unroll
+        for (int e = 0; e < N; ++e) sum[e] *= back;
+        most = m;
+        const float f = st.x == -INFINITY ? 0.0f : ex2(st.x - m), part = st.y * f;
+#pragma unroll 4
+        for (int i = 0; i < here; ++i) {
+            const float *o = p.part_o + cell_of(warp + (k0 + i) * kJoinWarps) * D + lane;
+            const float fi = __shfl_sync(0xFFFFFFFFu, f, i);
+            total += __shfl_sync(0xFFFFFFFFu, part, i);
+#pragma unroll
+            for (int e = 0; e < N; ++e) sum[e] = fmaf(o[32 * e], fi, sum[e]);
+        }
     }
 #pragma unroll
     for (int e = 0; e < N; ++e) held[warp][lane + 32 * e] = sum[e];
-    if (lane == 0) held[warp][D] = total;
+    if (lane == 0) {
+        held[warp][D] = total;
+        held[warp][D + 1] = most;
+    }
     __syncthreads();
     if (threadIdx.x < D / 4) {
+        float top_m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) top_m = fmaxf(top_m, held[w][D + 1]);
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         float all = 0.0f;
 #pragma unroll
         for (int w = 0; w < kJoinWarps; ++w) {
             const float *h = held[w] + threadIdx.x * 4;
-            v.x += h[0];
-            v.y += h[1];
-            v.z += h[2];
-            v.w += h[3];
-            all += held[w][D];
+            const float f = held[w][D + 1] == -INFINITY ? 0.0f : ex2(held[w][D + 1] - top_m);
+            v.x = fmaf(h[0], f, v.x);
+            v.y = fmaf(h[1], f, v.y);
+            v.z = fmaf(h[2], f, v.z);
+            v.w = fmaf(h[3], f, v.w);
+            all = fmaf(held[w][D], f, all);
         }
         store_row<E>(p, row, static_cast<int64_t>(head) * D + threadIdx.x * 4, v, all);
         if (threadIdx.x == 0 && p.lse) p.lse[row * p.q_heads + head] = finish_lse(top_m, all);
@@ -770,7 +808,7 @@ Plan plan(int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_
     const int resident = pl.n_tiles == 1 ? (head_dim == 64 ? kResident<64, 1> : head_dim == 128 ? kResident<128, 1> : kResident<256, 1>)
                                          : (head_dim == 64 ? kResident<64, 2> : head_dim == 128 ? kResident<128, 2> : 2);
     const int64_t slots = (int64_t)kSms * resident;
-    if (units >= 4 * slots || tiles <= 2 * kLeastShare) return pl;
+    if (units >= 4 * slots || tiles <= 2 * kLeastShare || units * tiles >= ((int64_t)1 << 31)) return pl;
     const int64_t most = (units * tiles + kLeastShare - 1) / kLeastShare;
     pl.ctas = (int32_t)(most < slots ? most : slots);
     return pl;
@@ -815,7 +853,7 @@ int64_t qknorm_kv4_attention_workspace_bytes(int64_t T, int32_t B, int32_t q_hea
     if ((int64_t)max_q_len * q_heads > kMaxRows) return -1;
     const Plan pl = plan(B, q_heads, kv_heads, head_dim, max_q_len, max_seq_len);
     // partial outputs and sums of every share's two ends, the pairs' first tiles
-    return pl.ctas == 0 ? 0 : (int64_t)pl.ctas * 2 * 8 * pl.n_tiles * (head_dim + 2) * 4 + (pl.pairs + 1) * 8;
+    return pl.ctas == 0 ? 0 : (int64_t)pl.ctas * 2 * 8 * pl.n_tiles * (head_dim + 2) * 4 + (pl.pairs + 1) * 4;
 }
 
 qkn_status qknorm_kv4_attention(const void *q, int64_t q_stride, void *out, int64_t out_stride, float *lse,
@@ -910,7 +948,7 @@ qkn_status qknorm_kv4_attention(const void *q, int64_t q_stride, void *out, int6
         const int64_t cells = (int64_t)pl.ctas * 2 * 8 * pl.n_tiles;
         p.part_o = static_cast<float *>(workspace);
         p.part_s = reinterpret_cast<float2 *>(p.part_o + cells * head_dim);
-        p.starts = reinterpret_cast<int64_t *>(p.part_s + cells);
+        p.starts = reinterpret_cast<int32_t *>(p.part_s + cells);
     }
     const int64_t tile_rows = 8 * pl.n_tiles, rows = (int64_t)max_q_len * p.group;
     const dim3 grid = p.shared ? dim3((unsigned)pl.ctas) : dim3((unsigned)(pl.row_tiles * kv_heads), (unsigned)B);
