@@ -286,6 +286,420 @@ __global__ void __launch_bounds__(kGradScalarWarps * 32) heads_grad_scalar_kerne
     }
 }
 
+// ----------------------------------------------------------------------------
+// Aligned heads: a head is held by p.lanes lanes (a power of two), each with
+// two 16-byte vectors placed so that a pair never leaves its lane: vectors u and
+// u + rotary_dim / 2 where pairs are (i, i + rotary_dim / 2), any two where they
+// are neighbours.  A warp takes 32 / lanes heads at a time of one token and one
+// tensor, U times, all loads first; the token's cosines and sines and the
+// tensor's gamma are loaded once for all of them.
+template <typename E>
+struct LanePlace {
+    int lo, hi;          // first elements of the two vectors
+    bool turn_lo, turn_hi;
+};
+template <typename E, typename P>
+__device__ __forceinline__ LanePlace<E> lane_place(const P &p, int u) {
+    constexpr int V = Elem<E>::kPerVec;
+    if (p.interleaved) {
+        const int lo = u * V, hi = p.head_dim / 2 + u * V;
+        return {lo, hi, lo < 2 * p.half, hi < 2 * p.half};
+    }
+    const int nr = p.half / V;
+    if (u < nr) return {u * V, p.half + u * V, true, true};
+    const int lo = 2 * p.half + 2 * (u - nr) * V;
+    return {lo, lo + V, false, false};
+}
+
+// The lane's cosines and sines: of its V pairs (lo[e], hi[e]), or with
+// neighbouring pairs of the V / 2 pairs of lo, then of hi.
+template <typename E, typename P>
+__device__ __forceinline__ void lane_turns(const P &p, const LanePlace<E> &at, const float *cs, float (&c)[Elem<E>::kPerVec],
+                                           float (&s)[Elem<E>::kPerVec]) {
+    constexpr int V = Elem<E>::kPerVec;
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+        const bool lo = !p.interleaved || i < V / 2;
+        const int pair = p.interleaved ? (lo ? at.lo / 2 + i : at.hi / 2 + i - V / 2) : at.lo + i;
+        if (cs && (lo ? at.turn_lo : at.turn_hi)) {
+            const float2 a = __ldg(reinterpret_cast<const float2 *>(cs + pair));
+            const float2 b = __ldg(reinterpret_cast<const float2 *>(cs + p.half + pair));
+            c[i] = a.x, c[i + 1] = a.y, s[i] = b.x, s[i + 1] = b.y;
+        } else {
+            c[i] = c[i + 1] = 1.0f, s[i] = s[i + 1] = 0.0f;
+        }
+    }
+}
+
+// Rotates the lane's elements in place (`back`: by the opposite angle).
+template <typename E, typename C>
+__device__ __forceinline__ void lane_rotate(bool interleaved, C (&a)[Elem<E>::kPerVec], C (&b)[Elem<E>::kPerVec],
+                                            const float (&c)[Elem<E>::kPerVec], const float (&s)[Elem<E>::kPerVec], C sign) {
+    constexpr int V = Elem<E>::kPerVec;
+    if (interleaved) {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const C x = a[2 * i], y = a[2 * i + 1], sn = static_cast<C>(s[i]) * sign, cn = static_cast<C>(c[i]);
+            a[2 * i] = x * cn - y * sn;
+            a[2 * i + 1] = x * sn + y * cn;
+            const C z = b[2 * i], w = b[2 * i + 1], sm = static_cast<C>(s[V / 2 + i]) * sign, cm = static_cast<C>(c[V / 2 + i]);
+            b[2 * i] = z * cm - w * sm;
+            b[2 * i + 1] = z * sm + w * cm;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const C x = a[i], y = b[i], sn = static_cast<C>(s[i]) * sign, cn = static_cast<C>(c[i]);
+            a[i] = x * cn - y * sn;
+            b[i] = x * sn + y * cn;
+        }
+    }
+}
+
+template <typename E, typename C>
+__device__ __forceinline__ void widen_to(const uint4 &v, C (&x)[Elem<E>::kPerVec]) {
+    F2 w[Elem<E>::kPerVec / 2];
+    Elem<E>::widen(v, w);
+#pragma unroll
+    for (int i = 0; i < Elem<E>::kPerVec / 2; ++i) {
+        x[2 * i] = static_cast<C>(f2_lo(w[i]));
+        x[2 * i + 1] = static_cast<C>(f2_hi(w[i]));
+    }
+}
+template <typename E>
+__device__ __forceinline__ uint4 narrow_from(const float (&x)[Elem<E>::kPerVec]) {
+    F2 w[Elem<E>::kPerVec / 2];
+#pragma unroll
+    for (int i = 0; i < Elem<E>::kPerVec / 2; ++i) w[i] = f2(x[2 * i], x[2 * i + 1]);
+    return Elem<E>::narrow(w);
+}
+// gamma of the lane's vector at element `at`, as floats.
+template <typename E>
+__device__ __forceinline__ void lane_gamma(const char *gamma, int at, float (&g)[Elem<E>::kPerVec]) {
+    using GE = typename Elem<E>::G;
+    constexpr int KG = Elem<E>::kGVecs, N = Elem<GE>::kPerVec;
+#pragma unroll
+    for (int v = 0; v < KG; ++v) {
+        float x[N];
+        widen_to<GE, float>(ld_gamma(gamma + static_cast<int64_t>(at) * sizeof(GE) + 16 * v), x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) g[v * N + i] = x[i];
+    }
+}
+__device__ __forceinline__ float lanes_sum(float v, int lanes) { return segment_sum(v, lanes); }
+__device__ __forceinline__ double lanes_sum(double v, int lanes) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        if (off < lanes) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+    return v;
+}
+
+// Norm and rotation of the lane's elements, in C.
+template <typename E, typename C>
+__device__ __forceinline__ void lane_forward(const RopeParams &p, bool norm, int turn, const float (&ga)[Elem<E>::kPerVec],
+                                             const float (&gb)[Elem<E>::kPerVec], const float (&c)[Elem<E>::kPerVec],
+                                             const float (&s)[Elem<E>::kPerVec], C (&a)[Elem<E>::kPerVec],
+                                             C (&b)[Elem<E>::kPerVec]) {
+    constexpr int V = Elem<E>::kPerVec;
+    if (norm) {
+        C even = C(0), odd = C(0);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            even = fma(a[i], a[i], even);
+            odd = fma(b[i], b[i], odd);
+        }
+        const C r = norm_factor(lanes_sum(even + odd, p.lanes), p);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            a[i] = a[i] * static_cast<C>(ga[i]) * r;
+            b[i] = b[i] * static_cast<C>(gb[i]) * r;
+        }
+    }
+    lane_rotate<E, C>(p.interleaved, a, b, c, s, C(1));
+    if (turn != kTurnRow) {
+        const C v = turn == kTurnPad ? C(0) : C(__uint_as_float(0x7FFFFFFFu));
+#pragma unroll
+        for (int i = 0; i < V; ++i) a[i] = b[i] = v;
+    }
+}
+
+// The lane's elements to codes and, by the first lanes, the groups' scales.
+template <int V>
+__device__ __forceinline__ void store_codes(uint8_t *codes, int at, const uint32_t (&c)[V]) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) w |= c[i] << (4 * i);
+    if constexpr (V == 8) *reinterpret_cast<uint32_t *>(codes + at / 2) = w;
+    else *reinterpret_cast<uint16_t *>(codes + at / 2) = static_cast<uint16_t>(w);
+}
+template <typename E>
+__device__ __forceinline__ void lane_quantise(const RopeParams &p, int u, bool store, const LanePlace<E> &at,
+                                              const double (&a)[Elem<E>::kPerVec], const double (&b)[Elem<E>::kPerVec],
+                                              uint8_t *codes, __half *scales) {
+    constexpr int V = Elem<E>::kPerVec;
+    double ma = 0.0, mb = 0.0;
+    bool bad_a = false, bad_b = false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        ma = fmax(ma, fabs(a[i]));
+        mb = fmax(mb, fabs(b[i]));
+        bad_a |= !isfinite(a[i]);
+        bad_b |= !isfinite(b[i]);
+    }
+    const int group_a = at.lo / kKv4Group, group_b = at.hi / kKv4Group, groups = p.head_dim / kKv4Group;
+    const int lane = threadIdx.x & 31;
+    const uint32_t seg = (p.lanes == 32 ? 0xFFFFFFFFu : ((1u << p.lanes) - 1u) << (lane & ~(p.lanes - 1)));
+    double sa = 0.0, sb = 0.0;
+    for (int g = 0; g < groups; ++g) {
+        double m = fmax(group_a == g ? ma : 0.0, group_b == g ? mb : 0.0);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            if (off < p.lanes) m = fmax(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+        const bool bad = (__ballot_sync(0xFFFFFFFFu, (group_a == g && bad_a) || (group_b == g && bad_b)) & seg) != 0;
+        const __half sh = kv4_scale(m, bad);
+        const double s = static_cast<double>(__half2float(sh));
+        if (group_a == g) sa = s;
+        if (group_b == g) sb = s;
+        if (store && u == g) scales[g] = sh;
+    }
+    uint32_t ca[V], cb[V];
+    const double ia = 1.0 / sa, ib = 1.0 / sb;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        ca[i] = sa > 0.0 ? kv4_code(a[i], sa, ia) : 8u;
+        cb[i] = sb > 0.0 ? kv4_code(b[i], sb, ib) : 8u;
+    }
+    if (store) {
+        store_codes<V>(codes, at.lo, ca);
+        store_codes<V>(codes, at.hi, cb);
+    }
+}
+
+constexpr int kVectorWarps = 8;
+
+template <typename E, int U, int SINK>
+__global__ void __launch_bounds__(kVectorWarps * 32) heads_vector_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int V = Elem<E>::kPerVec;
+    constexpr int kEsz = sizeof(typename Elem<E>::Bits);
+    pdl_wait_and_release();
+    const uint32_t item = blockIdx.x * kVectorWarps + (threadIdx.x >> 5);
+    const uint32_t t32 = item / static_cast<uint32_t>(p.chunks);
+    const int64_t t = t32;
+    if (t >= p.T) return;
+    int chunk = static_cast<int>(item - t32 * p.chunks);
+    const int lane = threadIdx.x & 31, u = lane & (p.lanes - 1), per = 32 / p.lanes, first = lane / p.lanes;
+    // which tensor: Q's chunks, then K's, then V's
+    int which = 0;
+    if (chunk >= p.chunks_of[0]) {
+        chunk -= p.chunks_of[0];
+        which = 1;
+        if (chunk >= p.chunks_of[1]) {
+            chunk -= p.chunks_of[1];
+            which = 2;
+        }
+    }
+    const int heads = p.heads[which];
+    const bool active = u < p.units;
+    const LanePlace<E> at = lane_place<E>(p, active ? u : 0);
+    const char *in = p.in[which] + t * p.stride[which];
+    const int head_bytes = p.head_dim * kEsz;
+
+    if (SINK == kSinkKv4 && which > 0) {  // one head of a lane group at a time, in 64 bits
+        const int h = chunk * per + first;
+        const bool there = active && h < heads;
+        uint4 va = make_uint4(0, 0, 0, 0), vb = va;
+        if (there) {
+            va = ld_stream(in + static_cast<int64_t>(h) * head_bytes + at.lo * kEsz);
+            vb = ld_stream(in + static_cast<int64_t>(h) * head_bytes + at.hi * kEsz);
+        }
+        const int64_t slot = p.slots[t];
+        if constexpr (SINK == kSinkKv4) {
+            double a[V], b[V];
+            widen_to<E, double>(va, a);
+            widen_to<E, double>(vb, b);
+            if (which == 1) {
+                const int64_t pos = p.positions[t];
+                const int turn = turn_of(pos, p.table_rows);
+                float c[V], s[V], ga[V] = {}, gb[V] = {};
+                lane_turns<E>(p, at, turn == kTurnRow ? p.table + pos * 2 * p.half : nullptr, c, s);
+                if (p.gamma[1]) {
+                    lane_gamma<E>(p.gamma[1], at.lo, ga);
+                    lane_gamma<E>(p.gamma[1], at.hi, gb);
+                }
+                lane_forward<E, double>(p, p.gamma[1] != nullptr, turn, ga, gb, c, s, a, b);
+            }
+            const bool store = there && slot >= 0 && slot < p.num_slots;
+            const int64_t page = store ? slot / p.page_size : 0;
+            const int64_t cell = (page * heads + h) * p.page_size + (store ? slot - page * p.page_size : 0);
+            const int kv = which - 1;
+            lane_quantise<E>(p, u, store, at, a, b, reinterpret_cast<uint8_t *>(p.cache[kv]) + cell * (p.head_dim / 2),
+                             p.scales[kv] + cell * (p.head_dim / kKv4Group));
+        }
+        return;
+    }
+
+    uint4 va[U], vb[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+        const int h = (chunk * U + j) * per + first;
+        va[j] = vb[j] = make_uint4(0, 0, 0, 0);
+        if (active && h < heads) {
+            va[j] = ld_stream(in + static_cast<int64_t>(h) * head_bytes + at.lo * kEsz);
+            vb[j] = ld_stream(in + static_cast<int64_t>(h) * head_bytes + at.hi * kEsz);
+        }
+    }
+    char *out;
+    int64_t step = head_bytes;
+    if (SINK == kSinkRows || which == 0) {
+        out = p.out[which] + t * p.stride[which];
+    } else {
+        const int64_t slot = p.slots[t];
+        if (slot < 0 || slot >= p.num_slots) return;
+        const int64_t page = slot / p.page_size, off = slot - page * p.page_size;
+        out = p.cache[which - 1] + page * p.page_stride[which - 1] + off * p.token_stride[which - 1];
+        step = p.head_stride[which - 1];
+        if (which == 2) {
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int h = (chunk * U + j) * per + first;
+                if (active && h < heads) {
+                    *reinterpret_cast<uint4 *>(out + h * step + at.lo * kEsz) = va[j];
+                    *reinterpret_cast<uint4 *>(out + h * step + at.hi * kEsz) = vb[j];
+                }
+            }
+            return;
+        }
+    }
+    const int64_t pos = p.positions[t];
+    const int turn = turn_of(pos, p.table_rows);
+    float c[V], s[V], ga[V] = {}, gb[V] = {};
+    lane_turns<E>(p, at, turn == kTurnRow ? p.table + pos * 2 * p.half : nullptr, c, s);
+    const char *gamma = p.gamma[which];
+    if (gamma) {
+        lane_gamma<E>(gamma, at.lo, ga);
+        lane_gamma<E>(gamma, at.hi, gb);
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+        const int h = (chunk * U + j) * per + first;
+        float a[V], b[V];
+        widen_to<E, float>(va[j], a);
+        widen_to<E, float>(vb[j], b);
+        lane_forward<E, float>(p, gamma != nullptr, turn, ga, gb, c, s, a, b);
+        if (active && h < heads) {
+            st_stream(out + h * step + at.lo * kEsz, narrow_from<E>(a));
+            st_stream(out + h * step + at.hi * kEsz, narrow_from<E>(b));
+        }
+    }
+}
+
+// Gradient of aligned heads: the same placing; CTAs stay and take tokens and
+// heads in turn, so that a lane keeps its elements' dgamma sums in registers,
+// first over Q's heads, then over K's; they are added over the warp's lane
+// groups, then over the warps in order.
+template <typename E, int U>
+__global__ void __launch_bounds__(kVectorWarps * 32) heads_grad_vector_kernel(const __grid_constant__ RopeGradParams p) {
+    constexpr int V = Elem<E>::kPerVec;
+    constexpr int kEsz = sizeof(typename Elem<E>::Bits);
+    pdl_wait_and_release();
+    extern __shared__ float sums[];  // [warps][head_dim]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int u = lane & (p.lanes - 1), per = 32 / p.lanes, first = lane / p.lanes;
+    const bool active = u < p.units;
+    const LanePlace<E> at = lane_place<E>(p, active ? u : 0);
+    const int head_bytes = p.head_dim * kEsz;
+    for (int w = 0; w < 2; ++w) {
+        float ga[V], gb[V], da[V] = {}, db[V] = {};
+        lane_gamma<E>(p.gamma[w], at.lo, ga);
+        lane_gamma<E>(p.gamma[w], at.hi, gb);
+        const int heads = p.heads[w];
+        const uint32_t chunks = (heads + per * U - 1) / (per * U);
+        const int64_t items = p.T * chunks;
+        for (int64_t item = static_cast<int64_t>(blockIdx.x) * kVectorWarps + warp; item < items;
+             item += static_cast<int64_t>(gridDim.x) * kVectorWarps) {
+            const uint32_t t32 = static_cast<uint32_t>(item) / chunks;
+            const int64_t t = t32;
+            const int chunk = static_cast<int>(static_cast<uint32_t>(item) - t32 * chunks);
+            uint4 xa[U], xb[U], ya[U], yb[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int h = (chunk * U + j) * per + first;
+                xa[j] = xb[j] = ya[j] = yb[j] = make_uint4(0, 0, 0, 0);
+                if (active && h < heads) {
+                    const char *x = p.x[w] + t * p.x_stride[w] + static_cast<int64_t>(h) * head_bytes;
+                    const char *y = p.dy[w] + t * p.dy_stride[w] + static_cast<int64_t>(h) * head_bytes;
+                    xa[j] = ld_stream(x + at.lo * kEsz);
+                    xb[j] = ld_stream(x + at.hi * kEsz);
+                    ya[j] = ld_stream(y + at.lo * kEsz);
+                    yb[j] = ld_stream(y + at.hi * kEsz);
+                }
+            }
+            const int64_t pos = p.positions[t];
+            const int turn = turn_of(pos, p.table_rows);
+            float c[V], s[V];
+            lane_turns<E>(p, at, turn == kTurnRow ? p.table + pos * 2 * p.half : nullptr, c, s);
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int h = (chunk * U + j) * per + first;
+                float a[V], b[V], ua[V], ub[V];
+                widen_to<E, float>(xa[j], a);
+                widen_to<E, float>(xb[j], b);
+                widen_to<E, float>(ya[j], ua);
+                widen_to<E, float>(yb[j], ub);
+                lane_rotate<E, float>(p.interleaved, ua, ub, c, s, -1.0f);
+                float S = 0.0f, M = 0.0f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    S = fmaf(a[i], a[i], S);
+                    S = fmaf(b[i], b[i], S);
+                    M = fmaf(ua[i] * ga[i], a[i], M);
+                    M = fmaf(ub[i] * gb[i], b[i], M);
+                }
+                S = lanes_sum(S, p.lanes);
+                M = lanes_sum(M, p.lanes);
+                const float r = rms_factor(S, p.inv_d, p.eps);
+                const float k = r * r * M * p.inv_d;
+                const bool there = active && h < heads;
+                const float past = __uint_as_float(0x7FFFFFFFu);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    float ea = ua[i] * a[i] * r, eb = ub[i] * b[i] * r;
+                    a[i] = r * (ua[i] * ga[i] - a[i] * k);
+                    b[i] = r * (ub[i] * gb[i] - b[i] * k);
+                    if (turn != kTurnRow) ea = eb = a[i] = b[i] = turn == kTurnPad ? 0.0f : past;
+                    da[i] += there ? ea : 0.0f;
+                    db[i] += there ? eb : 0.0f;
+                }
+                if (there) {
+                    char *dx = p.dx[w] + t * p.dx_stride[w] + static_cast<int64_t>(h) * head_bytes;
+                    st_stream(dx + at.lo * kEsz, narrow_from<E>(a));
+                    st_stream(dx + at.hi * kEsz, narrow_from<E>(b));
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            for (int off = p.lanes; off < 32; off <<= 1) {
+                da[i] += __shfl_xor_sync(0xFFFFFFFFu, da[i], off);
+                db[i] += __shfl_xor_sync(0xFFFFFFFFu, db[i], off);
+            }
+        if (first == 0 && active)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                sums[warp * p.head_dim + at.lo + i] = da[i];
+                sums[warp * p.head_dim + at.hi + i] = db[i];
+            }
+        __syncthreads();
+        for (int i = threadIdx.x; i < p.head_dim; i += kVectorWarps * 32) {
+            float v = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kVectorWarps; ++k) v += sums[k * p.head_dim + i];
+            p.partial[(static_cast<int64_t>(blockIdx.x) * 2 + w) * p.head_dim + i] = v;
+        }
+        __syncthreads();
+    }
+}
+
 // dgamma = the CTAs' partial sums added in CTA order: 8 lanes of rows per
 // column, combined in a fixed order.  `ctas` = 0 (no tokens) writes zeros.
 struct GradSumParams {
@@ -365,13 +779,49 @@ const void *scalar_kernel(int dt) {
     }
 }
 
+template <int SINK, int U>
+const void *vector_kernel(int dt) {
+    switch (dt) {
+        case QKN_F32: return (const void *)heads_vector_kernel<float, U, SINK>;
+        case QKN_BF16: return (const void *)heads_vector_kernel<__nv_bfloat16, U, SINK>;
+        case QKN_F16: return (const void *)heads_vector_kernel<__half, U, SINK>;
+        default:
+            if constexpr (SINK == kSinkKv4) return nullptr;
+            else return (const void *)heads_vector_kernel<__nv_fp8_e4m3, U, SINK>;
+    }
+}
+
+// Lanes of a head for the vector kernels; 0 where the sizes do not fit them.
+int vector_lanes(int dtype, int head_dim, int half) {
+    const int two = 2 * (16 / elem_bytes(dtype));  // elements of two vectors
+    if (head_dim % two != 0 || 2 * half % two != 0 || head_dim / two > 32) return 0;
+    int lanes = 1;
+    while (lanes < head_dim / two) lanes *= 2;
+    return lanes;
+}
+
 template <int SINK>
 qkn_status launch_heads(RopeParams &p, int dtype, bool aligned, void *stream) {
-    (void)aligned;
     int sms = 0;
     qkn_status st = device_sms(&sms);
     if (st != QKN_OK) return st;
     const int64_t rows = p.T * p.heads_total;
+    p.lanes = aligned ? vector_lanes(dtype, p.head_dim, p.half) : 0;
+    if (p.lanes > 0) {
+        p.units = p.head_dim / (2 * (16 / elem_bytes(dtype)));
+        const int per = 32 / p.lanes;
+        // four heads in flight per lane group once that leaves every SM warps enough
+        const int U = rows >= (int64_t)sms * 32 * per * 4 ? 4 : 1;
+        p.chunks = 0;
+        for (int i = 0; i < 3; ++i) {
+            const int n = per * (SINK == kSinkKv4 && i > 0 ? 1 : U);
+            p.chunks_of[i] = (p.heads[i] + n - 1) / n;
+            p.chunks += p.chunks_of[i];
+        }
+        const int64_t ctas = (p.T * p.chunks + kVectorWarps - 1) / kVectorWarps;
+        const void *fn = U == 4 ? vector_kernel<SINK, 4>(dtype) : vector_kernel<SINK, 1>(dtype);
+        return launched(launch_pdl(fn, dim3((unsigned)ctas), kVectorWarps * 32, 0, stream, p));
+    }
     int64_t grid = (rows + kScalarWarps - 1) / kScalarWarps;
     if (grid > 32 * static_cast<int64_t>(sms)) grid = 32 * static_cast<int64_t>(sms);
     return launched(launch_pdl(scalar_kernel<SINK>(dtype), dim3((unsigned)grid), kScalarWarps * 32, 0, stream, p));
@@ -820,15 +1270,29 @@ qkn_status qknorm_headwise_rope_backward(const void *q_in, int64_t q_stride, con
     const int64_t rows = T * ((int64_t)q_heads + k_heads);
     int64_t ctas = 0;
     if (T > 0) {
-        ctas = (rows + kGradScalarWarps - 1) / kGradScalarWarps;
+        p.lanes = aligned ? vector_lanes(dtype, head_dim, p.half) : 0;
+        const void *fn;
+        unsigned threads;
+        size_t smem;
+        if (p.lanes > 0) {
+            p.units = head_dim / (2 * (16 / esz));
+            const int64_t heads = (int64_t)kVectorWarps * (32 / p.lanes);
+            ctas = (rows + heads - 1) / heads;
+            threads = kVectorWarps * 32;
+            smem = (size_t)kVectorWarps * head_dim * 4;
+            fn = dtype == QKN_F32    ? (const void *)heads_grad_vector_kernel<float, 2>
+                 : dtype == QKN_BF16 ? (const void *)heads_grad_vector_kernel<__nv_bfloat16, 2>
+                                     : (const void *)heads_grad_vector_kernel<__half, 2>;
+        } else {
+            ctas = (rows + kGradScalarWarps - 1) / kGradScalarWarps;
+            threads = kGradScalarWarps * 32;
+            smem = (size_t)kGradScalarWarps * 2 * head_dim * 4;
+            fn = dtype == QKN_F32    ? (const void *)heads_grad_scalar_kernel<float>
+                 : dtype == QKN_BF16 ? (const void *)heads_grad_scalar_kernel<__nv_bfloat16>
+                                     : (const void *)heads_grad_scalar_kernel<__half>;
+        }
         if (ctas > grad_ctas(rows)) ctas = grad_ctas(rows);
-        const void *fn = dtype == QKN_F32    ? (const void *)heads_grad_scalar_kernel<float>
-                         : dtype == QKN_BF16 ? (const void *)heads_grad_scalar_kernel<__nv_bfloat16>
-                                             : (const void *)heads_grad_scalar_kernel<__half>;
-        (void)aligned;
-        if ((st = launched(launch_pdl(fn, dim3((unsigned)ctas), kGradScalarWarps * 32,
-                                      (size_t)kGradScalarWarps * 2 * head_dim * 4, stream, p))) != QKN_OK)
-            return st;
+        if ((st = launched(launch_pdl(fn, dim3((unsigned)ctas), threads, smem, stream, p))) != QKN_OK) return st;
     }
     GradSumParams g{};
     g.partial = p.partial;

@@ -35,7 +35,8 @@ struct RopeParams {
     int32_t interleaved;         // pairs (2i, 2i + 1) instead of (i, i + half)
     int32_t units;               // vector kernel: lanes of a head = head_dim / (2 * elements per vector)
     int32_t lanes;               // vector kernel: units rounded up to a power of two
-    int32_t chunks;              // vector kernel: warps per token
+    int32_t chunks;              // vector kernel: warps per token,
+    int32_t chunks_of[3];        // of which each tensor's
     float eps;
     float inv_d;                 // 1 / head_dim
     // caches (kSinkCache: bytes; kSinkKv4: codes, then scales)
