@@ -290,204 +290,444 @@ __global__ void __launch_bounds__(kGradScalarWarps * 32) heads_grad_scalar_kerne
 // Aligned heads: a head is held by p.lanes lanes (a power of two), each with
 // two 16-byte vectors placed so that a pair never leaves its lane: vectors u and
 // u + rotary_dim / 2 where pairs are (i, i + rotary_dim / 2), any two where they
-// are neighbours.  A warp takes 32 / lanes heads at a time of one token and one
-// tensor, U times, all loads first; the token's cosines and sines and the
-// tensor's gamma are loaded once for all of them.
+// are neighbours (those are sorted into first and second elements as they are
+// loaded, so that one code turns both).  A warp takes 32 / lanes heads at a time
+// of one token and one tensor, several times, the next heads' loads ahead of the
+// work on the ones at hand.  What the norm and the
+// rotation multiply an element by, but for r, is the same for all of them:
+//   a' = r (x_a (gamma_a cos) - x_b (gamma_b sin)),
+//   b' = r (x_a (gamma_a sin) + x_b (gamma_b cos)),
+// so those four factors of a pair are formed once, and a pair costs four packed
+// operations and one by r.
 template <typename E>
 struct LanePlace {
-    int lo, hi;          // first elements of the two vectors
-    bool turn_lo, turn_hi;
+    int lo, hi;            // first elements of the two vectors
+    int pair_lo, pair_hi;  // pairs of the first and second half of the lane's V pairs, negative: not turned
 };
 template <typename E, typename P>
 __device__ __forceinline__ LanePlace<E> lane_place(const P &p, int u) {
     constexpr int V = Elem<E>::kPerVec;
     if (p.interleaved) {
         const int lo = u * V, hi = p.head_dim / 2 + u * V;
-        return {lo, hi, lo < 2 * p.half, hi < 2 * p.half};
+        return {lo, hi, lo < 2 * p.half ? lo / 2 : -1, hi < 2 * p.half ? hi / 2 : -1};
     }
     const int nr = p.half / V;
-    if (u < nr) return {u * V, p.half + u * V, true, true};
+    if (u < nr) return {u * V, p.half + u * V, u * V, u * V + V / 2};
     const int lo = 2 * p.half + 2 * (u - nr) * V;
-    return {lo, lo + V, false, false};
+    return {lo, lo + V, -1, -1};
 }
 
-// The lane's cosines and sines: of its V pairs (lo[e], hi[e]), or with
-// neighbouring pairs of the V / 2 pairs of lo, then of hi.
+// Neighbouring pairs (x0, x1), (x2, x3), ..: a <- first elements, b <- second, and back.
+template <typename E>
+__device__ __forceinline__ void part_pairs(uint4 &a, uint4 &b) {
+    if constexpr (sizeof(typename Elem<E>::Bits) == 4) {
+        const uint4 x = a, y = b;
+        a = make_uint4(x.x, x.z, y.x, y.z);
+        b = make_uint4(x.y, x.w, y.y, y.w);
+    } else {
+        constexpr uint32_t first = sizeof(typename Elem<E>::Bits) == 2 ? 0x5410u : 0x6420u;
+        constexpr uint32_t second = sizeof(typename Elem<E>::Bits) == 2 ? 0x7632u : 0x7531u;
+        const uint4 x = a, y = b;
+        a = make_uint4(__byte_perm(x.x, x.y, first), __byte_perm(x.z, x.w, first), __byte_perm(y.x, y.y, first),
+                       __byte_perm(y.z, y.w, first));
+        b = make_uint4(__byte_perm(x.x, x.y, second), __byte_perm(x.z, x.w, second), __byte_perm(y.x, y.y, second),
+                       __byte_perm(y.z, y.w, second));
+    }
+}
+template <typename E>
+__device__ __forceinline__ void join_pairs(uint4 &a, uint4 &b) {
+    const uint4 x = a, y = b;
+    if constexpr (sizeof(typename Elem<E>::Bits) == 4) {
+        a = make_uint4(x.x, y.x, x.y, y.y);
+        b = make_uint4(x.z, y.z, x.w, y.w);
+    } else {
+        constexpr uint32_t low = sizeof(typename Elem<E>::Bits) == 2 ? 0x5410u : 0x5140u;
+        constexpr uint32_t high = sizeof(typename Elem<E>::Bits) == 2 ? 0x7632u : 0x7362u;
+        a = make_uint4(__byte_perm(x.x, y.x, low), __byte_perm(x.x, y.x, high), __byte_perm(x.y, y.y, low),
+                       __byte_perm(x.y, y.y, high));
+        b = make_uint4(__byte_perm(x.z, y.z, low), __byte_perm(x.z, y.z, high), __byte_perm(x.w, y.w, low),
+                       __byte_perm(x.w, y.w, high));
+    }
+}
+
+// Cosines and sines of the lane's V pairs (1 and 0 where it turns nothing).
 template <typename E, typename P>
 __device__ __forceinline__ void lane_turns(const P &p, const LanePlace<E> &at, const float *cs, float (&c)[Elem<E>::kPerVec],
                                            float (&s)[Elem<E>::kPerVec]) {
-    constexpr int V = Elem<E>::kPerVec;
+    constexpr int H = Elem<E>::kPerVec / 2;
 #pragma unroll
-    for (int i = 0; i < V; i += 2) {
-        const bool lo = !p.interleaved || i < V / 2;
-        const int pair = p.interleaved ? (lo ? at.lo / 2 + i : at.hi / 2 + i - V / 2) : at.lo + i;
-        if (cs && (lo ? at.turn_lo : at.turn_hi)) {
-            const float2 a = __ldg(reinterpret_cast<const float2 *>(cs + pair));
-            const float2 b = __ldg(reinterpret_cast<const float2 *>(cs + p.half + pair));
-            c[i] = a.x, c[i + 1] = a.y, s[i] = b.x, s[i + 1] = b.y;
+    for (int h = 0; h < 2; ++h) {
+        const int pair = h ? at.pair_hi : at.pair_lo;
+#pragma unroll
+        for (int i = 0; i < H; ++i) c[h * H + i] = 1.0f, s[h * H + i] = 0.0f;
+        if (pair < 0) continue;
+        if constexpr (H >= 4) {
+#pragma unroll
+            for (int i = 0; i < H; i += 4) {
+                const float4 x = __ldg(reinterpret_cast<const float4 *>(cs + pair + i));
+                const float4 y = __ldg(reinterpret_cast<const float4 *>(cs + p.half + pair + i));
+                c[h * H + i] = x.x, c[h * H + i + 1] = x.y, c[h * H + i + 2] = x.z, c[h * H + i + 3] = x.w;
+                s[h * H + i] = y.x, s[h * H + i + 1] = y.y, s[h * H + i + 2] = y.z, s[h * H + i + 3] = y.w;
+            }
         } else {
-            c[i] = c[i + 1] = 1.0f, s[i] = s[i + 1] = 0.0f;
+            const float2 x = __ldg(reinterpret_cast<const float2 *>(cs + pair));
+            const float2 y = __ldg(reinterpret_cast<const float2 *>(cs + p.half + pair));
+            c[h * H] = x.x, c[h * H + 1] = x.y, s[h * H] = y.x, s[h * H + 1] = y.y;
         }
     }
 }
 
-// Rotates the lane's elements in place (`back`: by the opposite angle).
-template <typename E, typename C>
-__device__ __forceinline__ void lane_rotate(bool interleaved, C (&a)[Elem<E>::kPerVec], C (&b)[Elem<E>::kPerVec],
-                                            const float (&c)[Elem<E>::kPerVec], const float (&s)[Elem<E>::kPerVec], C sign) {
-    constexpr int V = Elem<E>::kPerVec;
-    if (interleaved) {
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            const C x = a[2 * i], y = a[2 * i + 1], sn = static_cast<C>(s[i]) * sign, cn = static_cast<C>(c[i]);
-            a[2 * i] = x * cn - y * sn;
-            a[2 * i + 1] = x * sn + y * cn;
-            const C z = b[2 * i], w = b[2 * i + 1], sm = static_cast<C>(s[V / 2 + i]) * sign, cm = static_cast<C>(c[V / 2 + i]);
-            b[2 * i] = z * cm - w * sm;
-            b[2 * i + 1] = z * sm + w * cm;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const C x = a[i], y = b[i], sn = static_cast<C>(s[i]) * sign, cn = static_cast<C>(c[i]);
-            a[i] = x * cn - y * sn;
-            b[i] = x * sn + y * cn;
-        }
-    }
-}
-
-template <typename E, typename C>
-__device__ __forceinline__ void widen_to(const uint4 &v, C (&x)[Elem<E>::kPerVec]) {
+template <typename E>
+__device__ __forceinline__ void widen_floats(const uint4 &v, float (&x)[Elem<E>::kPerVec]) {
     F2 w[Elem<E>::kPerVec / 2];
     Elem<E>::widen(v, w);
 #pragma unroll
     for (int i = 0; i < Elem<E>::kPerVec / 2; ++i) {
-        x[2 * i] = static_cast<C>(f2_lo(w[i]));
-        x[2 * i + 1] = static_cast<C>(f2_hi(w[i]));
+        x[2 * i] = f2_lo(w[i]);
+        x[2 * i + 1] = f2_hi(w[i]);
     }
 }
+// gamma of the lane's first and second elements of its pairs.
 template <typename E>
-__device__ __forceinline__ uint4 narrow_from(const float (&x)[Elem<E>::kPerVec]) {
-    F2 w[Elem<E>::kPerVec / 2];
-#pragma unroll
-    for (int i = 0; i < Elem<E>::kPerVec / 2; ++i) w[i] = f2(x[2 * i], x[2 * i + 1]);
-    return Elem<E>::narrow(w);
-}
-// gamma of the lane's vector at element `at`, as floats.
-template <typename E>
-__device__ __forceinline__ void lane_gamma(const char *gamma, int at, float (&g)[Elem<E>::kPerVec]) {
+__device__ __forceinline__ void lane_gamma(const char *gamma, const LanePlace<E> &at, bool interleaved,
+                                           float (&ga)[Elem<E>::kPerVec], float (&gb)[Elem<E>::kPerVec]) {
     using GE = typename Elem<E>::G;
-    constexpr int KG = Elem<E>::kGVecs, N = Elem<GE>::kPerVec;
+    constexpr int V = Elem<E>::kPerVec, KG = Elem<E>::kGVecs, N = Elem<GE>::kPerVec;
 #pragma unroll
     for (int v = 0; v < KG; ++v) {
-        float x[N];
-        widen_to<GE, float>(ld_gamma(gamma + static_cast<int64_t>(at) * sizeof(GE) + 16 * v), x);
+        float x[N], y[N];
+        widen_floats<GE>(ld_gamma(gamma + static_cast<int64_t>(at.lo) * sizeof(GE) + 16 * v), x);
+        widen_floats<GE>(ld_gamma(gamma + static_cast<int64_t>(at.hi) * sizeof(GE) + 16 * v), y);
 #pragma unroll
-        for (int i = 0; i < N; ++i) g[v * N + i] = x[i];
+        for (int i = 0; i < N; ++i) ga[v * N + i] = x[i], gb[v * N + i] = y[i];
+    }
+    if (interleaved) {
+        float x[V], y[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = ga[i], y[i] = gb[i];
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            ga[i] = x[2 * i], gb[i] = x[2 * i + 1];
+            ga[V / 2 + i] = y[2 * i], gb[V / 2 + i] = y[2 * i + 1];
+        }
     }
 }
-__device__ __forceinline__ float lanes_sum(float v, int lanes) { return segment_sum(v, lanes); }
-__device__ __forceinline__ double lanes_sum(double v, int lanes) {
+// Over the lanes of a head: L of them, or `lanes` where L is 0.
+template <int L = 0, typename C>
+__device__ __forceinline__ C lanes_sum(C v, int lanes) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
-        if (off < lanes) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+        if (off < (L > 0 ? L : lanes)) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+    return v;
+}
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+    for (int off = L / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, off));
     return v;
 }
 
-// Norm and rotation of the lane's elements, in C.
-template <typename E, typename C>
-__device__ __forceinline__ void lane_forward(const RopeParams &p, bool norm, int turn, const float (&ga)[Elem<E>::kPerVec],
-                                             const float (&gb)[Elem<E>::kPerVec], const float (&c)[Elem<E>::kPerVec],
-                                             const float (&s)[Elem<E>::kPerVec], C (&a)[Elem<E>::kPerVec],
-                                             C (&b)[Elem<E>::kPerVec]) {
+// The factors of a lane's pairs: a' = x_a aa + x_b ab, b' = x_a ba + x_b bb.
+template <int N>
+struct PairFactors {
+    F2 aa[N], ab[N], ba[N], bb[N];
+};
+template <typename E>
+__device__ __forceinline__ PairFactors<Elem<E>::kPerVec / 2> pair_factors(const RopeParams &p, const LanePlace<E> &at,
+                                                                          const char *gamma, const float *cs) {
     constexpr int V = Elem<E>::kPerVec;
-    if (norm) {
-        C even = C(0), odd = C(0);
+    float c[V], s[V], ga[V], gb[V];
+    lane_turns<E>(p, at, cs, c, s);
+    if (gamma) {
+        lane_gamma<E>(gamma, at, p.interleaved, ga, gb);
+    } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            even = fma(a[i], a[i], even);
-            odd = fma(b[i], b[i], odd);
-        }
-        const C r = norm_factor(lanes_sum(even + odd, p.lanes), p);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            a[i] = a[i] * static_cast<C>(ga[i]) * r;
-            b[i] = b[i] * static_cast<C>(gb[i]) * r;
-        }
+        for (int i = 0; i < V; ++i) ga[i] = gb[i] = 1.0f;
     }
-    lane_rotate<E, C>(p.interleaved, a, b, c, s, C(1));
-    if (turn != kTurnRow) {
-        const C v = turn == kTurnPad ? C(0) : C(__uint_as_float(0x7FFFFFFFu));
+    PairFactors<V / 2> f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) a[i] = b[i] = v;
+    for (int i = 0; i < V / 2; ++i) {
+        f.aa[i] = f2(ga[2 * i] * c[2 * i], ga[2 * i + 1] * c[2 * i + 1]);
+        f.ab[i] = f2(-gb[2 * i] * s[2 * i], -gb[2 * i + 1] * s[2 * i + 1]);
+        f.ba[i] = f2(ga[2 * i] * s[2 * i], ga[2 * i + 1] * s[2 * i + 1]);
+        f.bb[i] = f2(gb[2 * i] * c[2 * i], gb[2 * i + 1] * c[2 * i + 1]);
+    }
+    return f;
+}
+
+// Whether the lane turns its pair i (of packed pairs: 2i and 2i + 1).  Elements
+// it does not turn are not mixed either: a neighbour's infinity stays there.
+template <typename E>
+__device__ __forceinline__ bool turned(const LanePlace<E> &at, int i, int n) {
+    return (i < n / 2 ? at.pair_lo : at.pair_hi) >= 0;
+}
+
+// One head: the lane's parted vectors to normed and turned elements.
+template <typename E, int L>
+__device__ __forceinline__ void lane_forward(const RopeParams &p, const LanePlace<E> &at, bool norm,
+                                             const PairFactors<Elem<E>::kPerVec / 2> &f, const uint4 &va, const uint4 &vb,
+                                             F2 (&a)[Elem<E>::kPerVec / 2], F2 (&b)[Elem<E>::kPerVec / 2]) {
+    constexpr int N = Elem<E>::kPerVec / 2;
+    F2 x[N], y[N];
+    Elem<E>::widen(va, x);
+    Elem<E>::widen(vb, y);
+    float r = 1.0f;
+    if (norm) {
+        F2 sum = mul2(x[0], x[0]), other = mul2(y[0], y[0]);
+#pragma unroll
+        for (int i = 1; i < N; ++i) {
+            sum = fma2(x[i], x[i], sum);
+            other = fma2(y[i], y[i], other);
+        }
+        r = rms_factor(lanes_sum<L>((f2_lo(sum) + f2_hi(sum)) + (f2_lo(other) + f2_hi(other)), p.lanes), p.inv_d, p.eps);
+    }
+    const F2 rr = f2(r, r);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        F2 fa = mul2(x[i], f.aa[i]), fb = mul2(y[i], f.bb[i]);
+        if (turned(at, i, N)) {
+            fa = fma2(y[i], f.ab[i], fa);
+            fb = fma2(x[i], f.ba[i], fb);
+        }
+        a[i] = mul2(fa, rr);
+        b[i] = mul2(fb, rr);
     }
 }
 
-// The lane's elements to codes and, by the first lanes, the groups' scales.
-template <int V>
-__device__ __forceinline__ void store_codes(uint8_t *codes, int at, const uint32_t (&c)[V]) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) w |= c[i] << (4 * i);
-    if constexpr (V == 8) *reinterpret_cast<uint32_t *>(codes + at / 2) = w;
-    else *reinterpret_cast<uint16_t *>(codes + at / 2) = static_cast<uint16_t>(w);
-}
+// ----------------------------------------------------------------------------
+// Codes (+ 8, in the low four bits) of a lane's pairs, packed and stored.
 template <typename E>
-__device__ __forceinline__ void lane_quantise(const RopeParams &p, int u, bool store, const LanePlace<E> &at,
-                                              const double (&a)[Elem<E>::kPerVec], const double (&b)[Elem<E>::kPerVec],
-                                              uint8_t *codes, __half *scales) {
+__device__ __forceinline__ void store_codes(bool interleaved, uint8_t *codes, const LanePlace<E> &at,
+                                            const uint32_t (&ca)[Elem<E>::kPerVec], const uint32_t (&cb)[Elem<E>::kPerVec]) {
     constexpr int V = Elem<E>::kPerVec;
-    double ma = 0.0, mb = 0.0;
-    bool bad_a = false, bad_b = false;
+    uint32_t lo = 0, hi = 0;
+    if (interleaved) {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            lo |= (ca[i] & 15u) << (8 * i) | (cb[i] & 15u) << (8 * i + 4);
+            hi |= (ca[V / 2 + i] & 15u) << (8 * i) | (cb[V / 2 + i] & 15u) << (8 * i + 4);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            lo |= (ca[i] & 15u) << (4 * i);
+            hi |= (cb[i] & 15u) << (4 * i);
+        }
+    }
+    if constexpr (V == 8) {
+        *reinterpret_cast<uint32_t *>(codes + at.lo / 2) = lo;
+        *reinterpret_cast<uint32_t *>(codes + at.hi / 2) = hi;
+    } else {
+        *reinterpret_cast<uint16_t *>(codes + at.lo / 2) = static_cast<uint16_t>(lo);
+        *reinterpret_cast<uint16_t *>(codes + at.hi / 2) = static_cast<uint16_t>(hi);
+    }
+}
+
+// Which of the head's two blocks (the lane's lo and hi vectors) element i of
+// the first (second = false) or second elements of its pairs lies in.
+template <typename E>
+__device__ __forceinline__ bool in_hi(bool interleaved, bool second, int i) {
+    return interleaved ? i >= Elem<E>::kPerVec / 2 : second;
+}
+
+// In 64 bits, from the rows again.
+template <typename E>
+__device__ __noinline__ void lane_quantise_exact(const RopeParams &p, int which, int turn, const float *cs, int u, bool store,
+                                                 LanePlace<E> at, uint4 va, uint4 vb, uint8_t *codes, __half *scales) {
+    constexpr int V = Elem<E>::kPerVec;
+    double a[V], b[V];
+    {
+        float x[V], y[V];
+        widen_floats<E>(va, x);
+        widen_floats<E>(vb, y);
+#pragma unroll
+        for (int i = 0; i < V; ++i) a[i] = x[i], b[i] = y[i];
+    }
+    if (which == 1) {
+        float c[V] = {}, s[V] = {};
+        if (turn == kTurnRow) lane_turns<E>(p, at, cs, c, s);
+        if (p.gamma[1]) {
+            double sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum = fma(a[i], a[i], fma(b[i], b[i], sum));
+            const double r = norm_factor(lanes_sum<0>(sum, p.lanes), p);
+            float ga[V], gb[V];
+            lane_gamma<E>(p.gamma[1], at, p.interleaved, ga, gb);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                a[i] *= static_cast<double>(ga[i]) * r;
+                b[i] *= static_cast<double>(gb[i]) * r;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const double x = a[i], y = b[i], cc = c[i], ss = s[i];
+            if (turned(at, i, V)) {
+                a[i] = x * cc - y * ss;
+                b[i] = x * ss + y * cc;
+            }
+            if (turn == kTurnPad) a[i] = b[i] = 0.0;
+            if (turn == kTurnPast) a[i] = b[i] = __uint_as_float(0x7FFFFFFFu);
+        }
+    }
+    double mlo = 0.0, mhi = 0.0;
+    bool bad_lo = false, bad_hi = false;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        ma = fmax(ma, fabs(a[i]));
-        mb = fmax(mb, fabs(b[i]));
-        bad_a |= !isfinite(a[i]);
-        bad_b |= !isfinite(b[i]);
+        const bool ha = in_hi<E>(p.interleaved, false, i), hb = in_hi<E>(p.interleaved, true, i);
+        mlo = fmax(mlo, fmax(ha ? 0.0 : fabs(a[i]), hb ? 0.0 : fabs(b[i])));
+        mhi = fmax(mhi, fmax(ha ? fabs(a[i]) : 0.0, hb ? fabs(b[i]) : 0.0));
+        bad_lo |= (!ha && !isfinite(a[i])) || (!hb && !isfinite(b[i]));
+        bad_hi |= (ha && !isfinite(a[i])) || (hb && !isfinite(b[i]));
     }
-    const int group_a = at.lo / kKv4Group, group_b = at.hi / kKv4Group, groups = p.head_dim / kKv4Group;
+    const int group_lo = at.lo / kKv4Group, group_hi = at.hi / kKv4Group, groups = p.head_dim / kKv4Group;
     const int lane = threadIdx.x & 31;
-    const uint32_t seg = (p.lanes == 32 ? 0xFFFFFFFFu : ((1u << p.lanes) - 1u) << (lane & ~(p.lanes - 1)));
-    double sa = 0.0, sb = 0.0;
+    const uint32_t seg = p.lanes == 32 ? 0xFFFFFFFFu : ((1u << p.lanes) - 1u) << (lane & ~(p.lanes - 1));
+    double slo = 0.0, shi = 0.0;
     for (int g = 0; g < groups; ++g) {
-        double m = fmax(group_a == g ? ma : 0.0, group_b == g ? mb : 0.0);
+        double m = fmax(group_lo == g ? mlo : 0.0, group_hi == g ? mhi : 0.0);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1)
             if (off < p.lanes) m = fmax(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
-        const bool bad = (__ballot_sync(0xFFFFFFFFu, (group_a == g && bad_a) || (group_b == g && bad_b)) & seg) != 0;
+        const bool bad = (__ballot_sync(0xFFFFFFFFu, (group_lo == g && bad_lo) || (group_hi == g && bad_hi)) & seg) != 0;
         const __half sh = kv4_scale(m, bad);
         const double s = static_cast<double>(__half2float(sh));
-        if (group_a == g) sa = s;
-        if (group_b == g) sb = s;
+        if (group_lo == g) slo = s;
+        if (group_hi == g) shi = s;
         if (store && u == g) scales[g] = sh;
     }
     uint32_t ca[V], cb[V];
-    const double ia = 1.0 / sa, ib = 1.0 / sb;
+    const double ilo = 1.0 / slo, ihi = 1.0 / shi;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        ca[i] = sa > 0.0 ? kv4_code(a[i], sa, ia) : 8u;
-        cb[i] = sb > 0.0 ? kv4_code(b[i], sb, ib) : 8u;
+        const bool ha = in_hi<E>(p.interleaved, false, i), hb = in_hi<E>(p.interleaved, true, i);
+        const double sa = ha ? shi : slo, sb = hb ? shi : slo;
+        ca[i] = sa > 0.0 ? kv4_code(a[i], sa, ha ? ihi : ilo) : 8u;
+        cb[i] = sb > 0.0 ? kv4_code(b[i], sb, hb ? ihi : ilo) : 8u;
     }
-    if (store) {
-        store_codes<V>(codes, at.lo, ca);
-        store_codes<V>(codes, at.hi, cb);
+    if (store) store_codes<E>(p.interleaved, codes, at, ca, cb);
+}
+
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ float max_abs(float m, F2 x) { return fmaxf(m, fmaxf(fabsf(f2_lo(x)), fabsf(f2_hi(x)))); }
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// In 32 bits.  With `formed` the elements carry the error of a norm and turn in
+// 32 bits, u = 2^-24: at most 10 u of the element (the squared sum's 11
+// additions halved, 4 for the root's 2 ulp, one for the last product) and 4 u of
+// the head's largest (two roundings of each product times |a cos| + |b sin| <=
+// sqrt(2) that largest, and one of their sum).  False, and nothing stored, where
+// a scale or a code lies nearer than that to a border, so that 64 bits have to
+// decide, or a scale is outside fp16's normal range.
+template <typename E, int L>
+__device__ __forceinline__ bool lane_quantise(const RopeParams &p, bool formed, int u, bool there, const LanePlace<E> &at,
+                                              const F2 (&a)[Elem<E>::kPerVec / 2], const F2 (&b)[Elem<E>::kPerVec / 2],
+                                              uint8_t *codes, __half *scales) {
+    constexpr int V = Elem<E>::kPerVec, N = V / 2, H = N / 2;
+    constexpr float kU = 5.9604645e-8f;
+    // largest of the first and second halves of the pairs' first and second elements
+    float m[4] = {};
+    F2 zero = f2(0.0f, 0.0f);  // NaN with any element that is not finite
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        m[i / H] = max_abs(m[i / H], a[i]);
+        m[2 + i / H] = max_abs(m[2 + i / H], b[i]);
+        zero = fma2(a[i], f2(0.0f, 0.0f), zero);
+        zero = fma2(b[i], f2(0.0f, 0.0f), zero);
     }
+    const bool inter = p.interleaved;
+    const float mlo = fmaxf(m[0], inter ? m[2] : m[1]), mhi = fmaxf(inter ? m[1] : m[2], m[3]);
+    const float err = formed ? 4.0f * kU * lanes_max<L>(fmaxf(mlo, mhi)) : 0.0f;
+    const float own = formed ? 10.0f * kU : 0.0f;
+    constexpr int groups = L * 2 * V / kKv4Group;  // the lanes hold the head exactly
+    const int group_lo = at.lo / kKv4Group, group_hi = at.hi / kKv4Group;
+    bool near = f2_lo(zero) != 0.0f || f2_hi(zero) != 0.0f;
+    float slo = 0.0f, shi = 0.0f;
+    __half held = __float2half(0.0f);
+#pragma unroll
+    for (int g = 0; g < groups; ++g) {
+        const float top = lanes_max<L>(fmaxf(group_lo == g ? mlo : 0.0f, group_hi == g ? mhi : 0.0f));
+        const float q = top * 0.142857149f;
+        // fp16 rounds at the middle of q's low 13 bits; kU q is at most one step of q, and q is off by
+        // three such steps besides top's error
+        const float steps = fabsf(static_cast<float>(static_cast<int>(__float_as_uint(q) & 0x1FFFu) - 0x1000));
+        if (top > 0.0f && (!(q >= 1.220703125e-4f && q < 65000.0f) || steps * (kU * q) <= err * 0.15f + (own + 3.0f * kU) * q))
+            near = true;
+        const __half sh = __float2half_rn(q);
+        const float s = __half2float(sh);
+        if (group_lo == g) slo = s;
+        if (group_hi == g) shi = s;
+        if (u == g) held = sh;
+    }
+    const float ilo = slo > 0.0f ? rcp_approx(slo) : 0.0f, ihi = shi > 0.0f ? rcp_approx(shi) : 0.0f;
+    const float ia1 = inter ? ihi : ilo, ib0 = inter ? ilo : ihi;
+    // + 1.5 * 2^23 + 8: the nearest integer, 8 added, in the low bits
+    const F2 magic = f2(12582920.0f, 12582920.0f), back = f2(-12582920.0f, -12582920.0f), minus = f2(-1.0f, -1.0f);
+    float d[4] = {};
+    uint32_t ca[V], cb[V];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float fa = i < H ? ilo : ia1, fb = i < H ? ib0 : ihi;
+        const F2 ta = mul2(a[i], f2(fa, fa)), tb = mul2(b[i], f2(fb, fb));
+        const F2 ka = add2(ta, magic), kb = add2(tb, magic);
+        d[i / H] = max_abs(d[i / H], fma2(add2(ka, back), minus, ta));
+        d[2 + i / H] = max_abs(d[2 + i / H], fma2(add2(kb, back), minus, tb));
+        ca[2 * i] = static_cast<uint32_t>(ka.v), ca[2 * i + 1] = static_cast<uint32_t>(ka.v >> 32);
+        cb[2 * i] = static_cast<uint32_t>(kb.v), cb[2 * i + 1] = static_cast<uint32_t>(kb.v >> 32);
+    }
+    // the reciprocal and the product move a quotient of at most 7.5 by less than 2e-6
+    const float dlo = fmaxf(d[0], inter ? d[2] : d[1]), dhi = fmaxf(inter ? d[1] : d[2], d[3]);
+    const bool edge = dlo > 0.5f - (err * ilo + 7.5f * own + 2e-6f) || dhi > 0.5f - (err * ihi + 7.5f * own + 2e-6f);
+    if (__any_sync(0xFFFFFFFFu, (near || (formed && edge)) && there)) return false;
+    if (!formed && edge) {
+        // elements as they came often lie on a border exactly: what is left of one after k scales is exact in
+        // 32 bits (at most 24 bits above the element's last) and decides; in a tie the even code
+        auto settle = [](uint32_t bits, float y, float scale) -> uint32_t {
+            const float k = __uint_as_float(bits) - 12582920.0f, left = fmaf(-k, scale, y), far = fabsf(left) - 0.5f * scale;
+            const bool move = far > 0.0f || (far == 0.0f && (bits & 1u));
+            return move ? (left > 0.0f ? bits + 1u : bits - 1u) : bits;
+        };
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float sa = i < H ? slo : (inter ? shi : slo), sb = i < H ? (inter ? slo : shi) : shi;
+            ca[2 * i] = settle(ca[2 * i], f2_lo(a[i]), sa);
+            ca[2 * i + 1] = settle(ca[2 * i + 1], f2_hi(a[i]), sa);
+            cb[2 * i] = settle(cb[2 * i], f2_lo(b[i]), sb);
+            cb[2 * i + 1] = settle(cb[2 * i + 1], f2_hi(b[i]), sb);
+        }
+    }
+    if (there) {
+        if (u < groups) scales[u] = held;
+        store_codes<E>(inter, codes, at, ca, cb);
+    }
+    return true;
 }
 
 constexpr int kVectorWarps = 8;
+constexpr int kManyHeads = 2;
 
-template <typename E, int U, int SINK>
+template <typename E, int SINK, int L>
 __global__ void __launch_bounds__(kVectorWarps * 32) heads_vector_kernel(const __grid_constant__ RopeParams p) {
     constexpr int V = Elem<E>::kPerVec;
     constexpr int kEsz = sizeof(typename Elem<E>::Bits);
+    constexpr bool kStay = SINK == kSinkKv4;  // whether a warp goes on to further heads
+    constexpr int U = kStay ? 1 : kManyHeads;  // heads of a lane group loaded at a time
     pdl_wait_and_release();
     const uint32_t item = blockIdx.x * kVectorWarps + (threadIdx.x >> 5);
     const uint32_t t32 = item / static_cast<uint32_t>(p.chunks);
     const int64_t t = t32;
     if (t >= p.T) return;
     int chunk = static_cast<int>(item - t32 * p.chunks);
-    const int lane = threadIdx.x & 31, u = lane & (p.lanes - 1), per = 32 / p.lanes, first = lane / p.lanes;
+    const int lanes = L > 0 ? L : p.lanes;
+    const int lane = threadIdx.x & 31, u = lane & (lanes - 1), per = 32 / lanes;
     // which tensor: Q's chunks, then K's, then V's
     int which = 0;
     if (chunk >= p.chunks_of[0]) {
@@ -498,202 +738,269 @@ __global__ void __launch_bounds__(kVectorWarps * 32) heads_vector_kernel(const _
             which = 2;
         }
     }
-    const int heads = p.heads[which];
-    const bool active = u < p.units;
+    const int first = chunk * p.chunk_heads, end = min(p.heads[which], first + p.chunk_heads);
+    const int h = first + lane / lanes;
+    const bool active = L > 0 || u < p.units;
     const LanePlace<E> at = lane_place<E>(p, active ? u : 0);
-    const char *in = p.in[which] + t * p.stride[which];
     const int head_bytes = p.head_dim * kEsz;
-
-    if (SINK == kSinkKv4 && which > 0) {  // one head of a lane group at a time, in 64 bits
-        const int h = chunk * per + first;
-        const bool there = active && h < heads;
-        uint4 va = make_uint4(0, 0, 0, 0), vb = va;
-        if (there) {
-            va = ld_stream(in + static_cast<int64_t>(h) * head_bytes + at.lo * kEsz);
-            vb = ld_stream(in + static_cast<int64_t>(h) * head_bytes + at.hi * kEsz);
-        }
-        const int64_t slot = p.slots[t];
-        if constexpr (SINK == kSinkKv4) {
-            double a[V], b[V];
-            widen_to<E, double>(va, a);
-            widen_to<E, double>(vb, b);
-            if (which == 1) {
-                const int64_t pos = p.positions[t];
-                const int turn = turn_of(pos, p.table_rows);
-                float c[V], s[V], ga[V] = {}, gb[V] = {};
-                lane_turns<E>(p, at, turn == kTurnRow ? p.table + pos * 2 * p.half : nullptr, c, s);
-                if (p.gamma[1]) {
-                    lane_gamma<E>(p.gamma[1], at.lo, ga);
-                    lane_gamma<E>(p.gamma[1], at.hi, gb);
-                }
-                lane_forward<E, double>(p, p.gamma[1] != nullptr, turn, ga, gb, c, s, a, b);
+    const char *in = p.in[which] + t * p.stride[which] + h * head_bytes;
+    uint4 va[U], vb[U], na[U], nb[U];  // the heads at hand, the next ones (kStay)
+    auto load = [&](uint4 (&a)[U], uint4 (&b)[U], int from) {  // heads from + j per, counted from h
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            a[j] = b[j] = make_uint4(0, 0, 0, 0);
+            if (active && h + from + j * per < end) {
+                a[j] = ld_stream(in + (from + j * per) * head_bytes + at.lo * kEsz);
+                b[j] = ld_stream(in + (from + j * per) * head_bytes + at.hi * kEsz);
             }
-            const bool store = there && slot >= 0 && slot < p.num_slots;
-            const int64_t page = store ? slot / p.page_size : 0;
-            const int64_t cell = (page * heads + h) * p.page_size + (store ? slot - page * p.page_size : 0);
-            const int kv = which - 1;
-            lane_quantise<E>(p, u, store, at, a, b, reinterpret_cast<uint8_t *>(p.cache[kv]) + cell * (p.head_dim / 2),
-                             p.scales[kv] + cell * (p.head_dim / kKv4Group));
+        }
+    };
+    load(va, vb, 0);
+    const int64_t pos = p.positions[t];
+    int64_t page = 0, off = 0;
+    if (SINK != kSinkRows && which > 0) {
+        const int64_t slot = p.slots[t];
+        if (slot < 0 || slot >= p.num_slots) return;
+        page = slot / p.page_size;
+        off = slot - page * p.page_size;
+    }
+    char *out = nullptr;
+    int64_t step = head_bytes;
+    if (SINK == kSinkRows || which == 0) {
+        out = p.out[which] + t * p.stride[which] + h * step;
+    } else if (SINK == kSinkCache) {
+        step = p.head_stride[which - 1];
+        out = p.cache[which - 1] + page * p.page_stride[which - 1] + off * p.token_stride[which - 1] + h * step;
+    }
+    const int turn = which == 2 ? static_cast<int>(kTurnRow) : turn_of(pos, p.table_rows);
+    const float *cs = p.table + (turn == kTurnRow && which < 2 ? pos * 2 * p.half : 0);
+    if (turn != kTurnRow && (SINK != kSinkKv4 || which == 0)) {  // zeros or NaN for all of the token's heads
+        F2 x[V / 2];
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const float v = turn == kTurnPad ? 0.0f : __uint_as_float(0x7FFFFFFFu);
+            x[i] = f2(v, v);
+        }
+        const uint4 w = Elem<E>::narrow(x);
+        for (int from = 0; active && h + from < end; from += per) {
+            const int64_t o = static_cast<int64_t>(from) * step;
+            st_stream(out + o + at.lo * kEsz, w);
+            st_stream(out + o + at.hi * kEsz, w);
         }
         return;
     }
-
-    uint4 va[U], vb[U];
+    const char *gamma = which < 2 ? p.gamma[which] : nullptr;
+    PairFactors<V / 2> f;
+    if (which < 2 && turn == kTurnRow) f = pair_factors<E>(p, at, gamma, cs);
+#pragma unroll 1
+    for (int from = 0; first + from < end; from += U * per) {
+        if (kStay && first + from + U * per < end) load(na, nb, from + U * per);
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-        const int h = (chunk * U + j) * per + first;
-        va[j] = vb[j] = make_uint4(0, 0, 0, 0);
-        if (active && h < heads) {
-            va[j] = ld_stream(in + static_cast<int64_t>(h) * head_bytes + at.lo * kEsz);
-            vb[j] = ld_stream(in + static_cast<int64_t>(h) * head_bytes + at.hi * kEsz);
-        }
-    }
-    char *out;
-    int64_t step = head_bytes;
-    if (SINK == kSinkRows || which == 0) {
-        out = p.out[which] + t * p.stride[which];
-    } else {
-        const int64_t slot = p.slots[t];
-        if (slot < 0 || slot >= p.num_slots) return;
-        const int64_t page = slot / p.page_size, off = slot - page * p.page_size;
-        out = p.cache[which - 1] + page * p.page_stride[which - 1] + off * p.token_stride[which - 1];
-        step = p.head_stride[which - 1];
-        if (which == 2) {
-#pragma unroll
-            for (int j = 0; j < U; ++j) {
-                const int h = (chunk * U + j) * per + first;
-                if (active && h < heads) {
-                    *reinterpret_cast<uint4 *>(out + h * step + at.lo * kEsz) = va[j];
-                    *reinterpret_cast<uint4 *>(out + h * step + at.hi * kEsz) = vb[j];
+        for (int j = 0; j < U; ++j) {
+            const int here = from + j * per;
+            const bool there = active && h + here < end;
+            const int64_t o = static_cast<int64_t>(here) * step;
+            if (SINK == kSinkCache && which == 2) {  // values as they are
+                if (there) {
+                    *reinterpret_cast<uint4 *>(out + o + at.lo * kEsz) = va[j];
+                    *reinterpret_cast<uint4 *>(out + o + at.hi * kEsz) = vb[j];
+                }
+                continue;
+            }
+            if (p.interleaved) part_pairs<E>(va[j], vb[j]);
+            F2 a[V / 2], b[V / 2];
+            if constexpr (SINK == kSinkKv4) {
+                if (which > 0) {
+                    const int kv = which - 1;
+                    const int64_t cell = (page * p.heads[1] + h + here) * p.page_size + off;
+                    uint8_t *codes = reinterpret_cast<uint8_t *>(p.cache[kv]) + cell * (p.head_dim / 2);
+                    __half *scales = p.scales[kv] + cell * (p.head_dim / kKv4Group);
+                    bool done = false;
+                    if (turn == kTurnRow) {
+                        if (kv == 0) {
+                            lane_forward<E, L>(p, at, gamma != nullptr, f, va[j], vb[j], a, b);
+                        } else {
+                            Elem<E>::widen(va[j], a);
+                            Elem<E>::widen(vb[j], b);
+                        }
+                        done = lane_quantise<E, L>(p, kv == 0, u, there, at, a, b, codes, scales);
+                    }
+                    if (!done) lane_quantise_exact<E>(p, which, turn, cs, u, there, at, va[j], vb[j], codes, scales);
+                    continue;
                 }
             }
-            return;
+            lane_forward<E, L>(p, at, gamma != nullptr, f, va[j], vb[j], a, b);
+            uint4 wa = Elem<E>::narrow(a), wb = Elem<E>::narrow(b);
+            if (p.interleaved) join_pairs<E>(wa, wb);
+            if (there) {
+                st_stream(out + o + at.lo * kEsz, wa);
+                st_stream(out + o + at.hi * kEsz, wb);
+            }
         }
-    }
-    const int64_t pos = p.positions[t];
-    const int turn = turn_of(pos, p.table_rows);
-    float c[V], s[V], ga[V] = {}, gb[V] = {};
-    lane_turns<E>(p, at, turn == kTurnRow ? p.table + pos * 2 * p.half : nullptr, c, s);
-    const char *gamma = p.gamma[which];
-    if (gamma) {
-        lane_gamma<E>(gamma, at.lo, ga);
-        lane_gamma<E>(gamma, at.hi, gb);
-    }
+        if (!kStay) break;
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-        const int h = (chunk * U + j) * per + first;
-        float a[V], b[V];
-        widen_to<E, float>(va[j], a);
-        widen_to<E, float>(vb[j], b);
-        lane_forward<E, float>(p, gamma != nullptr, turn, ga, gb, c, s, a, b);
-        if (active && h < heads) {
-            st_stream(out + h * step + at.lo * kEsz, narrow_from<E>(a));
-            st_stream(out + h * step + at.hi * kEsz, narrow_from<E>(b));
-        }
+        for (int j = 0; j < U; ++j) va[j] = na[j], vb[j] = nb[j];
     }
 }
 
-// Gradient of aligned heads: the same placing; CTAs stay and take tokens and
-// heads in turn, so that a lane keeps its elements' dgamma sums in registers,
-// first over Q's heads, then over K's; they are added over the warp's lane
-// groups, then over the warps in order.
-template <typename E, int U>
-__global__ void __launch_bounds__(kVectorWarps * 32) heads_grad_vector_kernel(const __grid_constant__ RopeGradParams p) {
-    constexpr int V = Elem<E>::kPerVec;
+// Gradient of aligned heads: the same placing; CTAs stay and take tokens in
+// turn, all heads of one tensor by a warp, so that a lane keeps its elements'
+// dgamma sums in registers, first over Q's heads, then over K's; they are added
+// over the warp's lane groups, then over the warps in order.
+constexpr int kGradWarps = 8;
+
+template <typename E, int L>
+__global__ void __launch_bounds__(kGradWarps * 32, 2) heads_grad_vector_kernel(const __grid_constant__ RopeGradParams p) {
+    constexpr int V = Elem<E>::kPerVec, N = V / 2;
     constexpr int kEsz = sizeof(typename Elem<E>::Bits);
     pdl_wait_and_release();
     extern __shared__ float sums[];  // [warps][head_dim]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int u = lane & (p.lanes - 1), per = 32 / p.lanes, first = lane / p.lanes;
-    const bool active = u < p.units;
+    const int lanes = L > 0 ? L : p.lanes;
+    const int u = lane & (lanes - 1), per = 32 / lanes, first = lane / lanes;
+    const bool active = L > 0 || u < p.units;
     const LanePlace<E> at = lane_place<E>(p, active ? u : 0);
     const int head_bytes = p.head_dim * kEsz;
     for (int w = 0; w < 2; ++w) {
-        float ga[V], gb[V], da[V] = {}, db[V] = {};
-        lane_gamma<E>(p.gamma[w], at.lo, ga);
-        lane_gamma<E>(p.gamma[w], at.hi, gb);
-        const int heads = p.heads[w];
-        const uint32_t chunks = (heads + per * U - 1) / (per * U);
-        const int64_t items = p.T * chunks;
-        for (int64_t item = static_cast<int64_t>(blockIdx.x) * kVectorWarps + warp; item < items;
-             item += static_cast<int64_t>(gridDim.x) * kVectorWarps) {
-            const uint32_t t32 = static_cast<uint32_t>(item) / chunks;
-            const int64_t t = t32;
-            const int chunk = static_cast<int>(static_cast<uint32_t>(item) - t32 * chunks);
-            uint4 xa[U], xb[U], ya[U], yb[U];
+        F2 ga[N], gb[N], da[N], db[N];
+        {
+            float x[V], y[V];
+            lane_gamma<E>(p.gamma[w], at, p.interleaved, x, y);
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-                const int h = (chunk * U + j) * per + first;
-                xa[j] = xb[j] = ya[j] = yb[j] = make_uint4(0, 0, 0, 0);
-                if (active && h < heads) {
-                    const char *x = p.x[w] + t * p.x_stride[w] + static_cast<int64_t>(h) * head_bytes;
-                    const char *y = p.dy[w] + t * p.dy_stride[w] + static_cast<int64_t>(h) * head_bytes;
-                    xa[j] = ld_stream(x + at.lo * kEsz);
-                    xb[j] = ld_stream(x + at.hi * kEsz);
-                    ya[j] = ld_stream(y + at.lo * kEsz);
-                    yb[j] = ld_stream(y + at.hi * kEsz);
-                }
+            for (int i = 0; i < N; ++i) {
+                ga[i] = f2(x[2 * i], x[2 * i + 1]);
+                gb[i] = f2(y[2 * i], y[2 * i + 1]);
+                da[i] = db[i] = f2(0.0f, 0.0f);
+            }
+        }
+        const int heads = p.heads[w], chunks = (heads + p.chunk_heads - 1) / p.chunk_heads;
+        const int64_t items = p.T * chunks;
+        for (int64_t item = static_cast<int64_t>(blockIdx.x) * kGradWarps + warp; item < items;
+             item += static_cast<int64_t>(gridDim.x) * kGradWarps) {
+            const uint32_t t32 = static_cast<uint32_t>(item) / static_cast<uint32_t>(chunks);
+            const int64_t t = t32;
+            const int begin = static_cast<int>(static_cast<uint32_t>(item) - t32 * chunks) * p.chunk_heads;
+            const int end = min(heads, begin + p.chunk_heads);
+            const char *x0 = p.x[w] + t * p.x_stride[w], *y0 = p.dy[w] + t * p.dy_stride[w];
+            char *dx = p.dx[w] + t * p.dx_stride[w];
+            uint4 xa = make_uint4(0, 0, 0, 0), xb = xa, ya = xa, yb = xa, nxa = xa, nxb = xa, nya = xa, nyb = xa;
+            int h = begin + first;
+            if (active && h < end) {
+                xa = ld_stream(x0 + h * head_bytes + at.lo * kEsz);
+                xb = ld_stream(x0 + h * head_bytes + at.hi * kEsz);
+                ya = ld_stream(y0 + h * head_bytes + at.lo * kEsz);
+                yb = ld_stream(y0 + h * head_bytes + at.hi * kEsz);
             }
             const int64_t pos = p.positions[t];
             const int turn = turn_of(pos, p.table_rows);
-            float c[V], s[V];
-            lane_turns<E>(p, at, turn == kTurnRow ? p.table + pos * 2 * p.half : nullptr, c, s);
+            if (turn != kTurnRow) {  // zero gradients, or NaN and NaN in dgamma
+                F2 bad[N];
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-                const int h = (chunk * U + j) * per + first;
-                float a[V], b[V], ua[V], ub[V];
-                widen_to<E, float>(xa[j], a);
-                widen_to<E, float>(xb[j], b);
-                widen_to<E, float>(ya[j], ua);
-                widen_to<E, float>(yb[j], ub);
-                lane_rotate<E, float>(p.interleaved, ua, ub, c, s, -1.0f);
-                float S = 0.0f, M = 0.0f;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    S = fmaf(a[i], a[i], S);
-                    S = fmaf(b[i], b[i], S);
-                    M = fmaf(ua[i] * ga[i], a[i], M);
-                    M = fmaf(ub[i] * gb[i], b[i], M);
+                for (int i = 0; i < N; ++i) {
+                    const float v = turn == kTurnPad ? 0.0f : __uint_as_float(0x7FFFFFFFu);
+                    bad[i] = f2(v, v);
                 }
-                S = lanes_sum(S, p.lanes);
-                M = lanes_sum(M, p.lanes);
-                const float r = rms_factor(S, p.inv_d, p.eps);
-                const float k = r * r * M * p.inv_d;
-                const bool there = active && h < heads;
-                const float past = __uint_as_float(0x7FFFFFFFu);
+                const uint4 v = Elem<E>::narrow(bad);
+                for (; active && h < end; h += per) {
+                    st_stream(dx + h * head_bytes + at.lo * kEsz, v);
+                    st_stream(dx + h * head_bytes + at.hi * kEsz, v);
+                    if (turn == kTurnPast)
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    float ea = ua[i] * a[i] * r, eb = ub[i] * b[i] * r;
-                    a[i] = r * (ua[i] * ga[i] - a[i] * k);
-                    b[i] = r * (ub[i] * gb[i] - b[i] * k);
-                    if (turn != kTurnRow) ea = eb = a[i] = b[i] = turn == kTurnPad ? 0.0f : past;
-                    da[i] += there ? ea : 0.0f;
-                    db[i] += there ? eb : 0.0f;
+                        for (int i = 0; i < N; ++i) da[i] = db[i] = bad[i];
                 }
+                continue;
+            }
+            F2 c[N], s[N], ns[N];
+            {
+                float cf[V], sf[V];
+                lane_turns<E>(p, at, p.table + pos * 2 * p.half, cf, sf);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    c[i] = f2(cf[2 * i], cf[2 * i + 1]);
+                    s[i] = f2(sf[2 * i], sf[2 * i + 1]);
+                    ns[i] = f2(-sf[2 * i], -sf[2 * i + 1]);
+                }
+            }
+#pragma unroll 1
+            for (int h0 = begin; h0 < end; h0 += per, h += per, xa = nxa, xb = nxb, ya = nya, yb = nyb) {
+                const bool there = active && h < end;
+                if (active && h + per < end) {
+                    nxa = ld_stream(x0 + (h + per) * head_bytes + at.lo * kEsz);
+                    nxb = ld_stream(x0 + (h + per) * head_bytes + at.hi * kEsz);
+                    nya = ld_stream(y0 + (h + per) * head_bytes + at.lo * kEsz);
+                    nyb = ld_stream(y0 + (h + per) * head_bytes + at.hi * kEsz);
+                }
+                if (p.interleaved) {
+                    part_pairs<E>(xa, xb);
+                    part_pairs<E>(ya, yb);
+                }
+                F2 a[N], b[N], ua[N], ub[N];
+                Elem<E>::widen(xa, a);
+                Elem<E>::widen(xb, b);
+                Elem<E>::widen(ya, ua);
+                Elem<E>::widen(yb, ub);
+                F2 S2 = f2(0.0f, 0.0f), M2 = S2;
+                F2 ea[N], eb[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    if (turned(at, i, N)) {
+                        const F2 y = ua[i];
+                        ua[i] = fma2(ub[i], s[i], mul2(y, c[i]));
+                        ub[i] = fma2(y, ns[i], mul2(ub[i], c[i]));
+                    }
+                    ea[i] = mul2(ua[i], a[i]);
+                    eb[i] = mul2(ub[i], b[i]);
+                    S2 = fma2(b[i], b[i], fma2(a[i], a[i], S2));
+                    M2 = fma2(eb[i], gb[i], fma2(ea[i], ga[i], M2));
+                }
+                const float S = lanes_sum<L>(f2_lo(S2) + f2_hi(S2), lanes), M = lanes_sum<L>(f2_lo(M2) + f2_hi(M2), lanes);
+                const float r = rms_factor(S, p.inv_d, p.eps), k = -(r * r) * M * p.inv_d;
+                const F2 rr = f2(r, r), kk = f2(k, k);
                 if (there) {
-                    char *dx = p.dx[w] + t * p.dx_stride[w] + static_cast<int64_t>(h) * head_bytes;
-                    st_stream(dx + at.lo * kEsz, narrow_from<E>(a));
-                    st_stream(dx + at.hi * kEsz, narrow_from<E>(b));
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        da[i] = fma2(ea[i], rr, da[i]);
+                        db[i] = fma2(eb[i], rr, db[i]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    a[i] = mul2(fma2(a[i], kk, mul2(ua[i], ga[i])), rr);
+                    b[i] = mul2(fma2(b[i], kk, mul2(ub[i], gb[i])), rr);
+                }
+                uint4 wa = Elem<E>::narrow(a), wb = Elem<E>::narrow(b);
+                if (p.interleaved) join_pairs<E>(wa, wb);
+                if (there) {
+                    st_stream(dx + h * head_bytes + at.lo * kEsz, wa);
+                    st_stream(dx + h * head_bytes + at.hi * kEsz, wb);
                 }
             }
         }
+        float xa[V], xb[V];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            xa[2 * i] = f2_lo(da[i]), xa[2 * i + 1] = f2_hi(da[i]);
+            xb[2 * i] = f2_lo(db[i]), xb[2 * i + 1] = f2_hi(db[i]);
+        }
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            for (int off = p.lanes; off < 32; off <<= 1) {
-                da[i] += __shfl_xor_sync(0xFFFFFFFFu, da[i], off);
-                db[i] += __shfl_xor_sync(0xFFFFFFFFu, db[i], off);
+            for (int off = lanes; off < 32; off <<= 1) {
+                xa[i] += __shfl_xor_sync(0xFFFFFFFFu, xa[i], off);
+                xb[i] += __shfl_xor_sync(0xFFFFFFFFu, xb[i], off);
             }
         if (first == 0 && active)
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                sums[warp * p.head_dim + at.lo + i] = da[i];
-                sums[warp * p.head_dim + at.hi + i] = db[i];
+            for (int i = 0; i < V; ++i) {  // element i of the pairs' firsts and seconds, back in its place
+                const int la = p.interleaved ? (i < V / 2 ? at.lo + 2 * i : at.hi + 2 * i - V) : at.lo + i;
+                const int lb = p.interleaved ? la + 1 : at.hi + i;
+                sums[warp * p.head_dim + la] = xa[i];
+                sums[warp * p.head_dim + lb] = xb[i];
             }
         __syncthreads();
-        for (int i = threadIdx.x; i < p.head_dim; i += kVectorWarps * 32) {
+        for (int i = threadIdx.x; i < p.head_dim; i += kGradWarps * 32) {
             float v = 0.0f;
 #pragma unroll
-            for (int k = 0; k < kVectorWarps; ++k) v += sums[k * p.head_dim + i];
+            for (int k = 0; k < kGradWarps; ++k) v += sums[k * p.head_dim + i];
             p.partial[(static_cast<int64_t>(blockIdx.x) * 2 + w) * p.head_dim + i] = v;
         }
         __syncthreads();
@@ -725,7 +1032,8 @@ __global__ void __launch_bounds__(32 * kSumRows) dgamma_sum_kernel(const __grid_
 }
 
 // ----------------------------------------------------------------------------
-// Cached tokens of the 4-bit cache back as rows: one thread per 8 elements.
+// Cached tokens of the 4-bit cache back as rows: one thread per 8 elements, a
+// row of threads along a token's K, then V elements.
 struct Kv4ReadParams {
     const uint8_t *codes[2];
     const __half *scales[2];
@@ -734,18 +1042,18 @@ struct Kv4ReadParams {
     const int64_t *slots;
     int64_t n, num_slots;
     int32_t page_size, heads, head_dim, words;  // words: 8-element words of a token's heads
+    int32_t vector;                             // rows are 16-byte aligned
 };
 template <typename E>
 __global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ Kv4ReadParams p) {
     pdl_wait_and_release();
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    const int64_t total = p.n * 2 * p.words;
-    if (i >= total) return;
-    const int64_t t = i / (2 * p.words);
-    int w = static_cast<int>(i - t * 2 * p.words);
-    const int kv = w >= p.words;
+    const uint32_t i = blockIdx.x * 256u + threadIdx.x, per_token = 2u * p.words;  // fewer than 2^32 threads
+    const uint32_t t = i / per_token;
+    if (t >= p.n) return;
+    uint32_t w = i - t * per_token;
+    const int kv = w >= static_cast<uint32_t>(p.words);
     w -= kv * p.words;
-    const int per_head = p.head_dim / 8, h = w / per_head, j = w - h * per_head;
+    const uint32_t per_head = p.head_dim / 8, h = w / per_head, j = w - h * per_head;
     const int64_t slot = p.slots[t];
     uint32_t codes = 0x88888888u;
     float s = 0.0f;
@@ -755,11 +1063,22 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ K
         codes = reinterpret_cast<const uint32_t *>(p.codes[kv])[cell * per_head + j];
         s = __half2float(p.scales[kv][cell * (p.head_dim / kKv4Group) + j * 8 / kKv4Group]);
     }
-    char *out = p.out[kv] + t * p.stride[kv];
+    float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float v = static_cast<float>(static_cast<int>((codes >> (4 * e)) & 15u) - 8) * s;
-        put_elem<E>(out, w * 8 + e, v);
+    for (int e = 0; e < 8; ++e) v[e] = static_cast<float>(static_cast<int>((codes >> (4 * e)) & 15u) - 8) * s;
+    char *out = p.out[kv] + t * p.stride[kv] + static_cast<int64_t>(w) * 8 * sizeof(typename Elem<E>::Bits);
+    if (p.vector) {
+        constexpr int V = Elem<E>::kPerVec;
+#pragma unroll
+        for (int k = 0; k < 8 / V; ++k) {
+            F2 x[V / 2];
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) x[e] = f2(v[k * V + 2 * e], v[k * V + 2 * e + 1]);
+            st_stream(out + 16 * k, Elem<E>::narrow(x));
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) put_elem<E>(out, e, v[e]);
     }
 }
 
@@ -779,16 +1098,35 @@ const void *scalar_kernel(int dt) {
     }
 }
 
-template <int SINK, int U>
-const void *vector_kernel(int dt) {
+// The kernels for heads of 64, 128 and 256 elements know their lanes; others
+// count them as they run (L = 0).
+template <typename E, int SINK>
+const void *vector_kernel(int lanes, bool exact) {
+    constexpr int k64 = 64 / (2 * Elem<E>::kPerVec);
+    if (exact && lanes == k64) return (const void *)heads_vector_kernel<E, SINK, k64>;
+    if (exact && lanes == 2 * k64) return (const void *)heads_vector_kernel<E, SINK, 2 * k64>;
+    if (exact && lanes == 4 * k64) return (const void *)heads_vector_kernel<E, SINK, 4 * k64>;
+    if constexpr (SINK == kSinkKv4) return nullptr;
+    else return (const void *)heads_vector_kernel<E, SINK, 0>;
+}
+template <int SINK>
+const void *vector_kernel(int dt, int lanes, bool exact) {
     switch (dt) {
-        case QKN_F32: return (const void *)heads_vector_kernel<float, U, SINK>;
-        case QKN_BF16: return (const void *)heads_vector_kernel<__nv_bfloat16, U, SINK>;
-        case QKN_F16: return (const void *)heads_vector_kernel<__half, U, SINK>;
+        case QKN_F32: return vector_kernel<float, SINK>(lanes, exact);
+        case QKN_BF16: return vector_kernel<__nv_bfloat16, SINK>(lanes, exact);
+        case QKN_F16: return vector_kernel<__half, SINK>(lanes, exact);
         default:
             if constexpr (SINK == kSinkKv4) return nullptr;
-            else return (const void *)heads_vector_kernel<__nv_fp8_e4m3, U, SINK>;
+            else return vector_kernel<__nv_fp8_e4m3, SINK>(lanes, exact);
     }
+}
+template <typename E>
+const void *grad_kernel(int lanes, bool exact) {
+    constexpr int k64 = 64 / (2 * Elem<E>::kPerVec);
+    if (exact && lanes == k64) return (const void *)heads_grad_vector_kernel<E, k64>;
+    if (exact && lanes == 2 * k64) return (const void *)heads_grad_vector_kernel<E, 2 * k64>;
+    if (exact && lanes == 4 * k64) return (const void *)heads_grad_vector_kernel<E, 4 * k64>;
+    return (const void *)heads_grad_vector_kernel<E, 0>;
 }
 
 // Lanes of a head for the vector kernels; 0 where the sizes do not fit them.
@@ -800,6 +1138,15 @@ int vector_lanes(int dtype, int head_dim, int half) {
     return lanes;
 }
 
+// How many times in a row a warp takes 32 / lanes heads of a token: once for
+// the fewest tokens, and up to 4 times (what is formed once for a token then
+// counts less) while that leaves every SM 64 warps' worth.
+int head_groups(int64_t rows, int per, int sms, int most) {
+    int n = 1;
+    while (n < most && rows >= (int64_t)sms * 64 * per * 2 * n) n *= 2;
+    return n;
+}
+
 template <int SINK>
 qkn_status launch_heads(RopeParams &p, int dtype, bool aligned, void *stream) {
     int sms = 0;
@@ -809,18 +1156,12 @@ qkn_status launch_heads(RopeParams &p, int dtype, bool aligned, void *stream) {
     p.lanes = aligned ? vector_lanes(dtype, p.head_dim, p.half) : 0;
     if (p.lanes > 0) {
         p.units = p.head_dim / (2 * (16 / elem_bytes(dtype)));
-        const int per = 32 / p.lanes;
-        // four heads in flight per lane group once that leaves every SM warps enough
-        const int U = rows >= (int64_t)sms * 32 * per * 4 ? 4 : 1;
+        p.chunk_heads = (32 / p.lanes) * head_groups(rows, 32 / p.lanes, sms, SINK == kSinkKv4 ? 4 : kManyHeads);
         p.chunks = 0;
-        for (int i = 0; i < 3; ++i) {
-            const int n = per * (SINK == kSinkKv4 && i > 0 ? 1 : U);
-            p.chunks_of[i] = (p.heads[i] + n - 1) / n;
-            p.chunks += p.chunks_of[i];
-        }
+        for (int i = 0; i < 3; ++i) p.chunks += p.chunks_of[i] = (p.heads[i] + p.chunk_heads - 1) / p.chunk_heads;
         const int64_t ctas = (p.T * p.chunks + kVectorWarps - 1) / kVectorWarps;
-        const void *fn = U == 4 ? vector_kernel<SINK, 4>(dtype) : vector_kernel<SINK, 1>(dtype);
-        return launched(launch_pdl(fn, dim3((unsigned)ctas), kVectorWarps * 32, 0, stream, p));
+        return launched(launch_pdl(vector_kernel<SINK>(dtype, p.lanes, p.lanes == p.units), dim3((unsigned)ctas),
+                                   kVectorWarps * 32, 0, stream, p));
     }
     int64_t grid = (rows + kScalarWarps - 1) / kScalarWarps;
     if (grid > 32 * static_cast<int64_t>(sms)) grid = 32 * static_cast<int64_t>(sms);
@@ -849,7 +1190,7 @@ qkn_status check_common(const Common &c, int64_t heads) {
     if (c.table_rows < 0 || c.table_rows >= ((int64_t)1 << 40))
         return fail(QKN_ERR_INVALID_ARG, "table_rows = %lld", (long long)c.table_rows);
     if (!(std::isfinite(c.eps) && c.eps >= 0.0f)) return fail(QKN_ERR_INVALID_ARG, "eps must be finite and >= 0");
-    if (heads < 1 || heads > (1 << 20)) return fail(QKN_ERR_INVALID_ARG, "%lld heads", (long long)heads);
+    if (heads < 1 || heads > (1 << 16)) return fail(QKN_ERR_INVALID_ARG, "%lld heads", (long long)heads);
     if (c.T > 0 && c.T >= ((int64_t)1 << 31) / heads) return fail(QKN_ERR_INVALID_ARG, "T * heads must stay below 2^31");
     if (c.T > 0 && (!c.positions || (!c.table && c.table_rows > 0 && c.rotary_dim > 0)))
         return fail(QKN_ERR_INVALID_ARG, "null positions or cos_sin");
@@ -1165,7 +1506,7 @@ qkn_status qknorm_kv4_read(const void *k_codes, const void *k_scales, const void
     Kv4ReadParams p{};
     p.words = (int32_t)(w / 8);
     const __int128 threads = (__int128)n * 2 * p.words;
-    if (threads > ((__int128)1 << 31) * 255) return fail(QKN_ERR_INVALID_ARG, "n * kv_heads * head_dim too large");
+    if (threads >= ((__int128)1 << 32) - 256) return fail(QKN_ERR_INVALID_ARG, "n * kv_heads * head_dim too large");
     const Span ws[] = {rows_span(k_out, w, k_stride, n, esz, "k_out"), rows_span(v_out, w, v_stride, n, esz, "v_out")};
     const Span rs[] = {num_pages ? flat(k_codes, codes, "k_codes") : flat(nullptr, 0, ""),
                        num_pages ? flat(k_scales, scales, "k_scales") : flat(nullptr, 0, ""),
@@ -1182,6 +1523,7 @@ qkn_status qknorm_kv4_read(const void *k_codes, const void *k_scales, const void
     p.stride[1] = v_stride * esz;
     p.slots = slots;
     p.n = n;
+    p.vector = aligned16(k_out) && aligned16(v_out) && p.stride[0] % 16 == 0 && p.stride[1] % 16 == 0;
     p.num_slots = num_pages * page_size;
     p.page_size = page_size;
     p.heads = kv_heads;
@@ -1195,7 +1537,7 @@ qkn_status qknorm_kv4_read(const void *k_codes, const void *k_scales, const void
 int64_t qknorm_headwise_rope_backward_workspace_bytes(int64_t T, int32_t q_heads, int32_t k_heads, int32_t head_dim) {
     if (T < 0 || q_heads < 1 || k_heads < 1 || head_dim < 1 || head_dim > kRopeMaxHeadDim) return -1;
     const int64_t heads = (int64_t)q_heads + k_heads;
-    if (heads > (1 << 20) || (T > 0 && T >= ((int64_t)1 << 31) / heads)) return -1;
+    if (heads > (1 << 16) || (T > 0 && T >= ((int64_t)1 << 31) / heads)) return -1;
     return grad_ctas(T * heads) * 2 * head_dim * 4;
 }
 
@@ -1276,13 +1618,20 @@ qkn_status qknorm_headwise_rope_backward(const void *q_in, int64_t q_stride, con
         size_t smem;
         if (p.lanes > 0) {
             p.units = head_dim / (2 * (16 / esz));
-            const int64_t heads = (int64_t)kVectorWarps * (32 / p.lanes);
-            ctas = (rows + heads - 1) / heads;
-            threads = kVectorWarps * 32;
-            smem = (size_t)kVectorWarps * head_dim * 4;
-            fn = dtype == QKN_F32    ? (const void *)heads_grad_vector_kernel<float, 2>
-                 : dtype == QKN_BF16 ? (const void *)heads_grad_vector_kernel<__nv_bfloat16, 2>
-                                     : (const void *)heads_grad_vector_kernel<__half, 2>;
+            int sms = 0;
+            if ((st = device_sms(&sms)) != QKN_OK) return st;
+            const int groups = head_groups(rows, 32 / p.lanes, sms, 4);
+            p.chunk_heads = (32 / p.lanes) * groups;
+            const int64_t items = T * (((int64_t)q_heads + p.chunk_heads - 1) / p.chunk_heads);  // Q's, the most
+            const int64_t k_items = T * (((int64_t)k_heads + p.chunk_heads - 1) / p.chunk_heads);
+            ctas = ((items > k_items ? items : k_items) + kGradWarps - 1) / kGradWarps;
+            if (ctas > 2 * (int64_t)sms) ctas = 2 * (int64_t)sms;  // what is resident
+            threads = kGradWarps * 32;
+            smem = (size_t)kGradWarps * head_dim * 4;
+            const bool exact = p.lanes == p.units;
+            fn = dtype == QKN_F32    ? grad_kernel<float>(p.lanes, exact)
+                 : dtype == QKN_BF16 ? grad_kernel<__nv_bfloat16>(p.lanes, exact)
+                                     : grad_kernel<__half>(p.lanes, exact);
         } else {
             ctas = (rows + kGradScalarWarps - 1) / kGradScalarWarps;
             threads = kGradScalarWarps * 32;

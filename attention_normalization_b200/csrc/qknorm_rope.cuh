@@ -36,7 +36,8 @@ struct RopeParams {
     int32_t units;               // vector kernel: lanes of a head = head_dim / (2 * elements per vector)
     int32_t lanes;               // vector kernel: units rounded up to a power of two
     int32_t chunks;              // vector kernel: warps per token,
-    int32_t chunks_of[3];        // of which each tensor's
+    int32_t chunks_of[3];        // of which each tensor's,
+    int32_t chunk_heads;         // and the heads of a warp
     float eps;
     float inv_d;                 // 1 / head_dim
     // caches (kSinkCache: bytes; kSinkKv4: codes, then scales)
@@ -66,6 +67,7 @@ struct RopeGradParams {
     int32_t interleaved;
     int32_t units;
     int32_t lanes;
+    int32_t chunk_heads;         // vector kernel: heads a warp takes of a token at a time
     float eps;
     float inv_d;
 };
