@@ -138,6 +138,38 @@ __device__ __forceinline__ int tensor_of(const RopeParams &p, int &h) {
     return 2;
 }
 
+// One head of K (which = 1) or V into the 4-bit cache by a whole warp, in 64
+// bits; `y` holds the head.  Out of line: the vector kernel comes here for the
+// few heads with a scale or code next to a border, and should not pay for it in
+// registers.
+template <typename E>
+__device__ __noinline__ void quantise_head(const RopeParams &p, int which, int64_t t, const char *row, double *y,
+                                           uint8_t *codes, __half *scales) {
+    const int lane = threadIdx.x & 31;
+    if (which == 1) {
+        const auto head = scalar_head<E, double>(p, row, p.gamma[1], t, lane);
+        head.each(lane, [&](int i, double v) { y[i] = v; });
+    } else {
+        for (int i = lane; i < p.head_dim; i += 32) y[i] = static_cast<double>(elem_at<E>(row, i));
+    }
+    __syncwarp();
+    for (int g = 0; g < p.head_dim / kKv4Group; ++g) {
+        const double a = y[g * kKv4Group + 2 * lane], b = y[g * kKv4Group + 2 * lane + 1];
+        double m = fmax(fabs(a), fabs(b));
+        const bool bad = __any_sync(0xFFFFFFFFu, !isfinite(a) || !isfinite(b));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        const __half sh = kv4_scale(m, bad);
+        const double s = static_cast<double>(__half2float(sh));
+        const bool zero = !(s > 0.0);
+        const double inv = 1.0 / s;
+        const uint32_t lo = zero ? 8u : kv4_code(a, s, inv), hi = zero ? 8u : kv4_code(b, s, inv);
+        codes[g * (kKv4Group / 2) + lane] = static_cast<uint8_t>(lo | (hi << 4));
+        if (lane == 0) scales[g] = sh;
+    }
+    __syncwarp();
+}
+
 constexpr int kScalarWarps = 8;
 
 template <typename E, int SINK>
@@ -175,31 +207,9 @@ __global__ void __launch_bounds__(kScalarWarps * 32) heads_scalar_kernel(const _
             }
         }
         if constexpr (SINK == kSinkKv4) {
-            double *y = held[warp];
-            if (which == 1) {
-                const auto head = scalar_head<E, double>(p, row, p.gamma[1], t, lane);
-                head.each(lane, [&](int i, double v) { y[i] = v; });
-            } else {
-                for (int i = lane; i < p.head_dim; i += 32) y[i] = static_cast<double>(elem_at<E>(row, i));
-            }
-            __syncwarp();
             const int64_t cell = (page * p.heads[1] + h) * p.page_size + off;
-            for (int g = 0; g < p.head_dim / kKv4Group; ++g) {
-                const double a = y[g * kKv4Group + 2 * lane], b = y[g * kKv4Group + 2 * lane + 1];
-                double m = fmax(fabs(a), fabs(b));
-                const bool bad = __any_sync(0xFFFFFFFFu, !isfinite(a) || !isfinite(b));
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-                const __half sh = kv4_scale(m, bad);
-                const double s = static_cast<double>(__half2float(sh));
-                const bool zero = !(s > 0.0);
-                const double inv = 1.0 / s;
-                const uint32_t lo = zero ? 8u : kv4_code(a, s, inv), hi = zero ? 8u : kv4_code(b, s, inv);
-                reinterpret_cast<uint8_t *>(p.cache[kv])[cell * (p.head_dim / 2) + g * (kKv4Group / 2) + lane] =
-                    static_cast<uint8_t>(lo | (hi << 4));
-                if (lane == 0) p.scales[kv][cell * (p.head_dim / kKv4Group) + g] = sh;
-            }
-            __syncwarp();
+            quantise_head<E>(p, which, t, row, held[warp], reinterpret_cast<uint8_t *>(p.cache[kv]) + cell * (p.head_dim / 2),
+                             p.scales[kv] + cell * (p.head_dim / kKv4Group));
         }
     }
 }
@@ -530,84 +540,6 @@ __device__ __forceinline__ bool in_hi(bool interleaved, bool second, int i) {
     return interleaved ? i >= Elem<E>::kPerVec / 2 : second;
 }
 
-// In 64 bits, from the rows again.
-template <typename E>
-__device__ __noinline__ void lane_quantise_exact(const RopeParams &p, int which, int turn, const float *cs, int u, bool store,
-                                                 LanePlace<E> at, uint4 va, uint4 vb, uint8_t *codes, __half *scales) {
-    constexpr int V = Elem<E>::kPerVec;
-    double a[V], b[V];
-    {
-        float x[V], y[V];
-        widen_floats<E>(va, x);
-        widen_floats<E>(vb, y);
-#pragma unroll
-        for (int i = 0; i < V; ++i) a[i] = x[i], b[i] = y[i];
-    }
-    if (which == 1) {
-        float c[V] = {}, s[V] = {};
-        if (turn == kTurnRow) lane_turns<E>(p, at, cs, c, s);
-        if (p.gamma[1]) {
-            double sum = 0.0;
-#pragma unroll
-            for (int i = 0; i < V; ++i) sum = fma(a[i], a[i], fma(b[i], b[i], sum));
-            const double r = norm_factor(lanes_sum<0>(sum, p.lanes), p);
-            float ga[V], gb[V];
-            lane_gamma<E>(p.gamma[1], at, p.interleaved, ga, gb);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                a[i] *= static_cast<double>(ga[i]) * r;
-                b[i] *= static_cast<double>(gb[i]) * r;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const double x = a[i], y = b[i], cc = c[i], ss = s[i];
-            if (turned(at, i, V)) {
-                a[i] = x * cc - y * ss;
-                b[i] = x * ss + y * cc;
-            }
-            if (turn == kTurnPad) a[i] = b[i] = 0.0;
-            if (turn == kTurnPast) a[i] = b[i] = __uint_as_float(0x7FFFFFFFu);
-        }
-    }
-    double mlo = 0.0, mhi = 0.0;
-    bool bad_lo = false, bad_hi = false;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const bool ha = in_hi<E>(p.interleaved, false, i), hb = in_hi<E>(p.interleaved, true, i);
-        mlo = fmax(mlo, fmax(ha ? 0.0 : fabs(a[i]), hb ? 0.0 : fabs(b[i])));
-        mhi = fmax(mhi, fmax(ha ? fabs(a[i]) : 0.0, hb ? fabs(b[i]) : 0.0));
-        bad_lo |= (!ha && !isfinite(a[i])) || (!hb && !isfinite(b[i]));
-        bad_hi |= (ha && !isfinite(a[i])) || (hb && !isfinite(b[i]));
-    }
-    const int group_lo = at.lo / kKv4Group, group_hi = at.hi / kKv4Group, groups = p.head_dim / kKv4Group;
-    const int lane = threadIdx.x & 31;
-    const uint32_t seg = p.lanes == 32 ? 0xFFFFFFFFu : ((1u << p.lanes) - 1u) << (lane & ~(p.lanes - 1));
-    double slo = 0.0, shi = 0.0;
-    for (int g = 0; g < groups; ++g) {
-        double m = fmax(group_lo == g ? mlo : 0.0, group_hi == g ? mhi : 0.0);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
-            if (off < p.lanes) m = fmax(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
-        const bool bad = (__ballot_sync(0xFFFFFFFFu, (group_lo == g && bad_lo) || (group_hi == g && bad_hi)) & seg) != 0;
-        const __half sh = kv4_scale(m, bad);
-        const double s = static_cast<double>(__half2float(sh));
-        if (group_lo == g) slo = s;
-        if (group_hi == g) shi = s;
-        if (store && u == g) scales[g] = sh;
-    }
-    uint32_t ca[V], cb[V];
-    const double ilo = 1.0 / slo, ihi = 1.0 / shi;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const bool ha = in_hi<E>(p.interleaved, false, i), hb = in_hi<E>(p.interleaved, true, i);
-        const double sa = ha ? shi : slo, sb = hb ? shi : slo;
-        ca[i] = sa > 0.0 ? kv4_code(a[i], sa, ha ? ihi : ilo) : 8u;
-        cb[i] = sb > 0.0 ? kv4_code(b[i], sb, hb ? ihi : ilo) : 8u;
-    }
-    if (store) store_codes<E>(p.interleaved, codes, at, ca, cb);
-}
-
 __device__ __forceinline__ F2 add2(F2 a, F2 b) {
     F2 d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
@@ -624,11 +556,12 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // 32 bits, u = 2^-24: at most 10 u of the element (the squared sum's 11
 // additions halved, 4 for the root's 2 ulp, one for the last product) and 4 u of
 // the head's largest (two roundings of each product times |a cos| + |b sin| <=
-// sqrt(2) that largest, and one of their sum).  False, and nothing stored, where
-// a scale or a code lies nearer than that to a border, so that 64 bits have to
-// decide, or a scale is outside fp16's normal range.
+// sqrt(2) that largest, and one of their sum).  Returns the lanes (as a mask) for
+// whose heads a scale or a code lies nearer than that to a border, so that 64
+// bits have to decide, or a scale is outside fp16's normal range; nothing of
+// those heads is stored.
 template <typename E, int L>
-__device__ __forceinline__ bool lane_quantise(const RopeParams &p, bool formed, int u, bool there, const LanePlace<E> &at,
+__device__ __forceinline__ uint32_t lane_quantise(const RopeParams &p, bool formed, int u, bool there, const LanePlace<E> &at,
                                               const F2 (&a)[Elem<E>::kPerVec / 2], const F2 (&b)[Elem<E>::kPerVec / 2],
                                               uint8_t *codes, __half *scales) {
     constexpr int V = Elem<E>::kPerVec, N = V / 2, H = N / 2;
@@ -686,7 +619,7 @@ __device__ __forceinline__ bool lane_quantise(const RopeParams &p, bool formed, 
     // the reciprocal and the product move a quotient of at most 7.5 by less than 2e-6
     const float dlo = fmaxf(d[0], inter ? d[2] : d[1]), dhi = fmaxf(inter ? d[1] : d[2], d[3]);
     const bool edge = dlo > 0.5f - (err * ilo + 7.5f * own + 2e-6f) || dhi > 0.5f - (err * ihi + 7.5f * own + 2e-6f);
-    if (__any_sync(0xFFFFFFFFu, (near || (formed && edge)) && there)) return false;
+    const uint32_t unsure = __ballot_sync(0xFFFFFFFFu, (near || (formed && edge)) && there);
     if (!formed && edge) {
         // elements as they came often lie on a border exactly: what is left of one after k scales is exact in
         // 32 bits (at most 24 bits above the element's last) and decides; in a tie the even code
@@ -704,18 +637,24 @@ __device__ __forceinline__ bool lane_quantise(const RopeParams &p, bool formed, 
             cb[2 * i + 1] = settle(cb[2 * i + 1], f2_hi(b[i]), sb);
         }
     }
-    if (there) {
+    const uint32_t mine = (L == 32 ? 0xFFFFFFFFu : (1u << L) - 1u) << ((threadIdx.x & 31) - u);
+    if (there && !(unsure & mine)) {
         if (u < groups) scales[u] = held;
         store_codes<E>(inter, codes, at, ca, cb);
     }
-    return true;
+    return unsure;
 }
 
-constexpr int kVectorWarps = 8;
+constexpr int kVectorWarps = 4;
 constexpr int kManyHeads = 2;
 
+// CTAs of an SM that the registers are kept low enough for: what the loads of
+// so short-lived warps need to overlap.
+template <typename E, int SINK>
+constexpr int kVectorResident = SINK == kSinkKv4 ? 5 : sizeof(typename Elem<E>::Bits) == 1 ? 4 : 7;
+
 template <typename E, int SINK, int L>
-__global__ void __launch_bounds__(kVectorWarps * 32) heads_vector_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kVectorWarps * 32, kVectorResident<E, SINK>) heads_vector_kernel(const __grid_constant__ RopeParams p) {
     constexpr int V = Elem<E>::kPerVec;
     constexpr int kEsz = sizeof(typename Elem<E>::Bits);
     constexpr bool kStay = SINK == kSinkKv4;  // whether a warp goes on to further heads
@@ -815,7 +754,7 @@ __global__ void __launch_bounds__(kVectorWarps * 32) heads_vector_kernel(const _
                     const int64_t cell = (page * p.heads[1] + h + here) * p.page_size + off;
                     uint8_t *codes = reinterpret_cast<uint8_t *>(p.cache[kv]) + cell * (p.head_dim / 2);
                     __half *scales = p.scales[kv] + cell * (p.head_dim / kKv4Group);
-                    bool done = false;
+                    uint32_t unsure = 0xFFFFFFFFu;
                     if (turn == kTurnRow) {
                         if (kv == 0) {
                             lane_forward<E, L>(p, at, gamma != nullptr, f, va[j], vb[j], a, b);
@@ -823,9 +762,20 @@ __global__ void __launch_bounds__(kVectorWarps * 32) heads_vector_kernel(const _
                             Elem<E>::widen(va[j], a);
                             Elem<E>::widen(vb[j], b);
                         }
-                        done = lane_quantise<E, L>(p, kv == 0, u, there, at, a, b, codes, scales);
+                        unsure = lane_quantise<E, L>(p, kv == 0, u, there, at, a, b, codes, scales);
                     }
-                    if (!done) lane_quantise_exact<E>(p, which, turn, cs, u, there, at, va[j], vb[j], codes, scales);
+                    if (unsure) {
+                        __shared__ double exact[kVectorWarps][L * 2 * V];
+                        for (int k = 0; k < 32 / L; ++k) {
+                            const int head = first + here + k;
+                            if (head >= end || !(unsure >> (k * L) & (L == 32 ? 0xFFFFFFFFu : (1u << L) - 1u))) continue;
+                            const int64_t at_cell = (page * p.heads[1] + head) * p.page_size + off;
+                            quantise_head<E>(p, which, t, p.in[which] + t * p.stride[which] + head * head_bytes,
+                                             exact[threadIdx.x >> 5],
+                                             reinterpret_cast<uint8_t *>(p.cache[kv]) + at_cell * (p.head_dim / 2),
+                                             p.scales[kv] + at_cell * (p.head_dim / kKv4Group));
+                        }
+                    }
                     continue;
                 }
             }
@@ -837,9 +787,12 @@ __global__ void __launch_bounds__(kVectorWarps * 32) heads_vector_kernel(const _
                 st_stream(out + o + at.hi * kEsz, wb);
             }
         }
-        if (!kStay) break;
+        if constexpr (kStay) {
 #pragma unroll
-        for (int j = 0; j < U; ++j) va[j] = na[j], vb[j] = nb[j];
+            for (int j = 0; j < U; ++j) va[j] = na[j], vb[j] = nb[j];
+        } else {
+            break;
+        }
     }
 }
 
