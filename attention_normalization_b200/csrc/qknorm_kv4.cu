@@ -11,6 +11,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "qknorm.h"
 #include "qknorm_checks.cuh"
 #include "qknorm_kernels.cuh"
@@ -819,8 +821,15 @@ qkn_status launch_attention(const Kv4AttnParams &p, dim3 grid, dim3 join_grid, v
     constexpr size_t smem = (size_t)kAttnWarps * Kv4Tile<D>::kRing;
     static_assert((size_t)8 * NT * (D + 2) * 4 <= Kv4Tile<D>::kRing, "a warp's partial result must fit its ring");
     const void *fn = (const void *)kv4_attention_kernel<E, D, NT>;
-    if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (smem > 48 * 1024) {  // once for each device; setting it again does no harm
+        static std::atomic<uint64_t> set{0};
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        const uint64_t bit = uint64_t(1) << (dev & 63);
+        if (e == cudaSuccess && (dev > 63 || !(set.load(std::memory_order_relaxed) & bit))) {
+            e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e == cudaSuccess) set.fetch_or(bit, std::memory_order_relaxed);
+        }
         if (e != cudaSuccess) return launched(e);
     }
     qkn_status st = launched(launch_pdl(fn, grid, kAttnWarps * 32, smem, stream, p));

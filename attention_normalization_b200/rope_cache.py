@@ -18,36 +18,56 @@ from typing import NamedTuple
 
 import torch
 
-from . import _DTYPES, _clib, _on, _out_like, _rows, _same, _stream_handle, _vec, capi, gamma_dtype
+from . import _DTYPES, _clib, _on, _rows, _same, _stream_handle, capi, gamma_dtype
+
+# These calls are short on the GPU, so their checks are kept few and flat: each
+# operand is looked at once, and what is made here is not looked at again.
 
 
-def _ints(t, name, n, dtype, device):
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == device and t.dtype == dtype and t.is_contiguous()
-            and t.numel() == n):
-        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of {n} elements on {device}")
+def _like(t, name, dev, dt):
+    """(T, width, row stride) of the rows `t`, on `dev` and of type `dt`."""
+    if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype != dt:
+        _rows(t, name)
+        _same(dev, dt, t, name)
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D [T, width]")
+    T, W = shape
+    if stride[1] != 1 and T > 0 and W > 1:
+        raise ValueError(f"{name} rows must be unit-stride along the width")
+    return T, W, (stride[0] if T > 1 else max(stride[0], W))
+
+
+def _match(t, name, like, T, W, stride=None):
+    """Row stride of the [T, W] rows `t` on the device and of the type of
+    `like`, which has to be `stride` where that is given."""
+    To, Wo, s = _like(t, name, like.device, like.dtype)
+    if To != T or Wo != W:
+        raise ValueError(f"{name} must be [{T}, {W}]")
+    if stride is not None and s != stride and T > 1:
+        raise ValueError(f"{name} must match its input's row stride")
+    return s
+
+
+def _flat(t, name, n, dtype, dev):
+    """Pointer of a contiguous tensor of `n` elements."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of {n} elements on {dev}")
     return t.data_ptr()
 
 
-def _table(cos_sin, positions, T, device):
-    if not (isinstance(cos_sin, torch.Tensor) and cos_sin.is_cuda and cos_sin.device == device
-            and cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.is_contiguous()):
-        raise ValueError(f"cos_sin must be a contiguous float32 CUDA tensor [table_rows, rotary_dim] on {device}")
-    return [cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1]], _ints(positions, "positions", T, torch.int64, device)
+def _table(cos_sin, dev):
+    if not isinstance(cos_sin, torch.Tensor) or cos_sin.dtype != torch.float32 or cos_sin.device != dev \
+            or len(cos_sin.shape) != 2 or not cos_sin.is_contiguous():
+        raise ValueError(f"cos_sin must be a contiguous float32 CUDA tensor [table_rows, rotary_dim] on {dev}")
+    P, rot = cos_sin.shape
+    return cos_sin.data_ptr(), P, rot
 
 
 def _heads(width, head_dim, name):
     if head_dim < 1 or width % head_dim:
         raise ValueError(f"{name}: the row width must be a whole number of heads of head_dim elements")
     return width // head_dim
-
-
-def _rows_like(t, name, like, shape):
-    """Stride of `t`, rows of `shape` on the device and of the type of `like`."""
-    _same(like.device, like.dtype, t, name)
-    To, W, s = _rows(t, name)
-    if (To, W) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}")
-    return s
 
 
 def _used_on(stream, *tensors):
@@ -58,16 +78,6 @@ def _used_on(stream, *tensors):
             t.record_stream(stream)
 
 
-def _out_rows(out, name, like, shape, stride, stream):
-    if out is None:
-        out = _out_like(like, stride)
-        _used_on(stream, out)
-        return out
-    if _rows_like(out, name, like, shape) != stride and shape[0] > 1:
-        raise ValueError(f"{name} must match its input's shape and row stride")
-    return out
-
-
 def qknorm_headwise_rope(q_in: torch.Tensor, k_in: torch.Tensor, gamma_q: torch.Tensor, gamma_k: torch.Tensor,
                          head_dim: int, cos_sin: torch.Tensor, positions: torch.Tensor, eps: float = 1e-6, *,
                          interleaved: bool = False, q_out=None, k_out=None, stream=None):
@@ -75,21 +85,29 @@ def qknorm_headwise_rope(q_in: torch.Tensor, k_in: torch.Tensor, gamma_q: torch.
     launch; returns ``(q_out, k_out)``.  ``interleaved`` rotates the pairs
     ``(2i, 2i + 1)`` instead of ``(i, i + rotary_dim / 2)``."""
     T, Wq, sq = _rows(q_in, "q_in")
-    Tk, Wk, sk = _rows(k_in, "k_in")
+    dev, dt = q_in.device, q_in.dtype
+    Tk, Wk, sk = _like(k_in, "k_in", dev, dt)
     if T != Tk:
         raise ValueError("q_in and k_in must have the same number of tokens")
-    dev, dt = q_in.device, q_in.dtype
-    _same(dev, dt, k_in, "k_in")
-    hq, hk = _heads(Wq, head_dim, "q_in"), _heads(Wk, head_dim, "k_in")
-    table, pos = _table(cos_sin, positions, T, dev)
-    q_out = _out_rows(q_out, "q_out", q_in, (T, Wq), sq, stream)
-    k_out = _out_rows(k_out, "k_out", k_in, (T, Wk), sk, stream)
+    table, P, rot = _table(cos_sin, dev)
+    pos = _flat(positions, "positions", T, torch.int64, dev)
     gdt = gamma_dtype(dt)
+    gq, gk = _flat(gamma_q, "gamma_q", head_dim, gdt, dev), _flat(gamma_k, "gamma_k", head_dim, gdt, dev)
+    if q_out is None:
+        q_out = q_in.new_empty_strided((T, Wq), (sq, 1))
+        _used_on(stream, q_out)
+    else:
+        _match(q_out, "q_out", q_in, T, Wq, sq)
+    if k_out is None:
+        k_out = k_in.new_empty_strided((T, Wk), (sk, 1))
+        _used_on(stream, k_out)
+    else:
+        _match(k_out, "k_out", k_in, T, Wk, sk)
     with _on(dev):
         st = capi().qknorm_headwise_rope(
-            q_in.data_ptr(), q_out.data_ptr(), _vec(gamma_q, "gamma_q", head_dim, gdt, dev), sq, hq,
-            k_in.data_ptr(), k_out.data_ptr(), _vec(gamma_k, "gamma_k", head_dim, gdt, dev), sk, hk, T, head_dim,
-            *table, int(interleaved), pos, float(eps), _DTYPES[dt], _stream_handle(stream, dev))
+            q_in.data_ptr(), q_out.data_ptr(), gq, sq, _heads(Wq, head_dim, "q_in"), k_in.data_ptr(), k_out.data_ptr(),
+            gk, sk, _heads(Wk, head_dim, "k_in"), T, head_dim, table, P, rot, 1 if interleaved else 0, pos, eps,
+            _DTYPES[dt], _stream_handle(stream, dev))
     _clib.check(st, "qknorm_headwise_rope")
     return q_out, k_out
 
@@ -102,13 +120,11 @@ def rope_backward_workspace_bytes(T: int, q_heads: int, k_heads: int, head_dim: 
     return n
 
 
-def _workspace(workspace, need, dev):
-    if workspace is None:
-        return torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
-    if not (isinstance(workspace, torch.Tensor) and workspace.is_cuda and workspace.device == dev
-            and workspace.is_contiguous()):
+def _workspace(workspace, dev):
+    """Pointer and bytes of a caller's workspace."""
+    if not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous CUDA tensor on {dev}")
-    return workspace
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def qknorm_headwise_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q_in: torch.Tensor, k_in: torch.Tensor,
@@ -120,70 +136,87 @@ def qknorm_headwise_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q_
     ``(dq_in, dk_in, dgamma_q, dgamma_k)``, the last two fp32 ``[head_dim]``
     summed over tokens and heads (overwritten, not accumulated)."""
     T, Wq, sq = _rows(q_in, "q_in")
-    Tk, Wk, sk = _rows(k_in, "k_in")
+    dev, dt = q_in.device, q_in.dtype
+    Tk, Wk, sk = _like(k_in, "k_in", dev, dt)
     if T != Tk:
         raise ValueError("q_in and k_in must have the same number of tokens")
-    dev, dt = q_in.device, q_in.dtype
-    _same(dev, dt, k_in, "k_in")
     hq, hk = _heads(Wq, head_dim, "q_in"), _heads(Wk, head_dim, "k_in")
-    table, pos = _table(cos_sin, positions, T, dev)
-    dqs, dks = _rows_like(dq_out, "dq_out", q_in, (T, Wq)), _rows_like(dk_out, "dk_out", k_in, (T, Wk))
-    fresh = []
+    table, P, rot = _table(cos_sin, dev)
+    pos = _flat(positions, "positions", T, torch.int64, dev)
+    gdt, f32 = gamma_dtype(dt), torch.float32
+    gq, gk = _flat(gamma_q, "gamma_q", head_dim, gdt, dev), _flat(gamma_k, "gamma_k", head_dim, gdt, dev)
+    dqs, dks = _match(dq_out, "dq_out", q_in, T, Wq), _match(dk_out, "dk_out", k_in, T, Wk)
+    made = []
     if dq_in is None:
-        fresh.append(dq_in := torch.empty((T, Wq), dtype=dt, device=dev))
+        made.append(dq_in := q_in.new_empty((T, Wq)))
+        dqi = Wq
+    else:
+        dqi = _match(dq_in, "dq_in", q_in, T, Wq)
     if dk_in is None:
-        fresh.append(dk_in := torch.empty((T, Wk), dtype=dt, device=dev))
-    dqi, dki = _rows_like(dq_in, "dq_in", q_in, (T, Wq)), _rows_like(dk_in, "dk_in", k_in, (T, Wk))
-    if dgamma_q is None:
-        fresh.append(dgamma_q := torch.empty((head_dim,), dtype=torch.float32, device=dev))
-    if dgamma_k is None:
-        fresh.append(dgamma_k := torch.empty((head_dim,), dtype=torch.float32, device=dev))
-    need = capi().qknorm_headwise_rope_backward_workspace_bytes(T, hq, hk, head_dim)
+        made.append(dk_in := k_in.new_empty((T, Wk)))
+        dki = Wk
+    else:
+        dki = _match(dk_in, "dk_in", k_in, T, Wk)
+    if dgamma_q is None and dgamma_k is None:
+        dgamma_q, dgamma_k = made_g = cos_sin.new_empty((2, head_dim)).unbind(0)
+        made += made_g
+    elif dgamma_q is None:
+        made.append(dgamma_q := cos_sin.new_empty((head_dim,)))
+    elif dgamma_k is None:
+        made.append(dgamma_k := cos_sin.new_empty((head_dim,)))
+    pgq, pgk = _flat(dgamma_q, "dgamma_q", head_dim, f32, dev), _flat(dgamma_k, "dgamma_k", head_dim, f32, dev)
+    lib = capi()
     if workspace is None:
-        fresh.append(workspace := _workspace(None, need, dev))
-    workspace = _workspace(workspace, need, dev)
-    _used_on(stream, *fresh)
-    gdt = gamma_dtype(dt)
-    f32 = torch.float32
+        need = lib.qknorm_headwise_rope_backward_workspace_bytes(T, hq, hk, head_dim)
+        made.append(workspace := cos_sin.new_empty((max(need, 16) // 4,)))
+        ws, ws_bytes = workspace.data_ptr(), max(need, 16)
+    else:
+        ws, ws_bytes = _workspace(workspace, dev)
+    _used_on(stream, *made)
     with _on(dev):
-        st = capi().qknorm_headwise_rope_backward(
-            q_in.data_ptr(), sq, dq_out.data_ptr(), dqs, dq_in.data_ptr(), dqi,
-            _vec(gamma_q, "gamma_q", head_dim, gdt, dev), _vec(dgamma_q, "dgamma_q", head_dim, f32, dev), hq,
-            k_in.data_ptr(), sk, dk_out.data_ptr(), dks, dk_in.data_ptr(), dki,
-            _vec(gamma_k, "gamma_k", head_dim, gdt, dev), _vec(dgamma_k, "dgamma_k", head_dim, f32, dev), hk,
-            T, head_dim, *table, int(interleaved), pos, float(eps), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _DTYPES[dt], _stream_handle(stream, dev))
+        st = lib.qknorm_headwise_rope_backward(
+            q_in.data_ptr(), sq, dq_out.data_ptr(), dqs, dq_in.data_ptr(), dqi, gq, pgq, hq,
+            k_in.data_ptr(), sk, dk_out.data_ptr(), dks, dk_in.data_ptr(), dki, gk, pgk, hk,
+            T, head_dim, table, P, rot, 1 if interleaved else 0, pos, eps, ws, ws_bytes, _DTYPES[dt],
+            _stream_handle(stream, dev))
     _clib.check(st, "qknorm_headwise_rope_backward")
     return dq_in, dk_in, dgamma_q, dgamma_k
 
 
 # --------------------------------------------------------------------------- paged caches
 
+_Strides = ctypes.c_int64 * 3
+
+
 def _append_rows(q_in, k_in, v_in, gamma_q, gamma_k, head_dim, cos_sin, positions, q_out, interleaved, stream):
     """The arguments the two append calls share, the query output and T, kv heads."""
     T, Wk, sk = _rows(k_in, "k_in")
     dev, dt = k_in.device, k_in.dtype
-    sv = _rows_like(v_in, "v_in", k_in, (T, Wk))
+    sv = _match(v_in, "v_in", k_in, T, Wk)
     hk = _heads(Wk, head_dim, "k_in")
-    table, pos = _table(cos_sin, positions, T, dev)
-    gdt = gamma_dtype(dt)
+    table, P, rot = _table(cos_sin, dev)
+    pos = _flat(positions, "positions", T, torch.int64, dev)
     if (gamma_k is None) != (gamma_q is None) and q_in is not None:
         raise ValueError("gamma_q and gamma_k: both (norm and rotation) or neither (rotation only)")
-    gq, gk = (None if g is None else _vec(g, name, head_dim, gdt, dev)
-              for g, name in ((gamma_q, "gamma_q"), (gamma_k, "gamma_k")))
+    gdt = gamma_dtype(dt)
+    gq = None if gamma_q is None else _flat(gamma_q, "gamma_q", head_dim, gdt, dev)
+    gk = None if gamma_k is None else _flat(gamma_k, "gamma_k", head_dim, gdt, dev)
     if q_in is None:
-        qp, qo, sq, hq = None, None, 0, 0
+        qp, qo, sq, hq, q_out = None, None, 0, 0, None
     else:
-        _same(dev, dt, q_in, "q_in")
-        Tq, Wq, sq = _rows(q_in, "q_in")
+        Tq, Wq, sq = _like(q_in, "q_in", dev, dt)
         if Tq != T:
             raise ValueError("q_in and k_in must have the same number of tokens")
         hq = _heads(Wq, head_dim, "q_in")
-        q_out = _out_rows(q_out, "q_out", q_in, (T, Wq), sq, stream)
+        if q_out is None:
+            q_out = q_in.new_empty_strided((T, Wq), (sq, 1))
+            _used_on(stream, q_out)
+        else:
+            _match(q_out, "q_out", q_in, T, Wq, sq)
         qp, qo = q_in.data_ptr(), q_out.data_ptr()
-    args = [qp, qo, gq, sq, hq, k_in.data_ptr(), gk, sk, v_in.data_ptr(), sv, hk, T, head_dim, *table,
-            int(interleaved), pos]
-    return args, q_out if q_in is not None else None, T, hk
+    args = (qp, qo, gq, sq, hq, k_in.data_ptr(), gk, sk, v_in.data_ptr(), sv, hk, T, head_dim, table, P, rot,
+            1 if interleaved else 0, pos)
+    return args, q_out, T, hk
 
 
 def qknorm_rope_append(q_in, k_in: torch.Tensor, v_in: torch.Tensor, gamma_q, gamma_k, head_dim: int,
@@ -201,19 +234,21 @@ def qknorm_rope_append(q_in, k_in: torch.Tensor, v_in: torch.Tensor, gamma_q, ga
     args, q_out, T, hk = _append_rows(q_in, k_in, v_in, gamma_q, gamma_k, head_dim, cos_sin, positions, q_out,
                                       interleaved, stream)
     dev = k_in.device
-    shapes, strides = [], []
+    dt = k_in.dtype
+    pages = k_cache.shape[:2]
+    strides = []
     for c, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _same(dev, k_in.dtype, c, name)
-        if c.dim() != 4 or tuple(c.shape[2:]) != (hk, head_dim) or (head_dim > 1 and c.stride(3) != 1):
+        _same(dev, dt, c, name)
+        shape, stride = c.shape, c.stride()
+        if len(shape) != 4 or shape[2] != hk or shape[3] != head_dim or (head_dim > 1 and stride[3] != 1):
             raise ValueError(f"{name} must be [pages, page_size, {hk}, {head_dim}] with unit stride along the last")
-        shapes.append((c.shape[0], c.shape[1]))
-        strides.append((ctypes.c_int64 * 3)(*c.stride()[:3]))
-    if shapes[0] != shapes[1]:
-        raise ValueError("k_cache and v_cache must have the same pages")
-    s = _ints(slots, "slots", T, torch.int64, dev)
+        if shape[:2] != pages:
+            raise ValueError("k_cache and v_cache must have the same pages")
+        strides.append(_Strides(*stride[:3]))
+    s = _flat(slots, "slots", T, torch.int64, dev)
     with _on(dev):
-        st = capi().qknorm_rope_append(*args, k_cache.data_ptr(), strides[0], v_cache.data_ptr(), strides[1],
-                                       *shapes[0], s, float(eps), _DTYPES[k_in.dtype], _stream_handle(stream, dev))
+        st = capi().qknorm_rope_append(*args, k_cache.data_ptr(), strides[0], v_cache.data_ptr(), strides[1], *pages, s,
+                                       eps, _DTYPES[dt], _stream_handle(stream, dev))
     _clib.check(st, "qknorm_rope_append")
     return q_out
 
@@ -244,16 +279,14 @@ def kv4_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int, devi
 def _kv4_args(cache, dev):
     """The cache's pointers and ``(num_pages, page_size, kv_heads, head_dim)``."""
     kc, ks, vc, vs = cache
-    for t, name, dt in ((kc, "k_codes", torch.uint8), (ks, "k_scales", torch.float16), (vc, "v_codes", torch.uint8),
-                        (vs, "v_scales", torch.float16)):
-        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == dev and t.dtype == dt and t.dim() == 4
-                and t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous 4-D CUDA {dt} tensor on {dev}")
-    pages, hk, ps, half = kc.shape
-    if vc.shape != kc.shape or ks.shape != vs.shape or tuple(ks.shape) != (pages, hk, ps, half * 2 // 64):
+    pages, hk, ps, half = shape = kc.shape
+    n = pages * hk * ps
+    ptrs = (_flat(kc, "k_codes", n * half, torch.uint8, dev), _flat(ks, "k_scales", n * half // 32, torch.float16, dev),
+            _flat(vc, "v_codes", n * half, torch.uint8, dev), _flat(vs, "v_scales", n * half // 32, torch.float16, dev))
+    if vc.shape != shape or ks.shape != vs.shape or ks.shape != (pages, hk, ps, half // 32):
         raise ValueError("the cache's codes must be [pages, kv_heads, page_size, head_dim / 2] and its scales "
                          "[pages, kv_heads, page_size, head_dim / 64]")
-    return [t.data_ptr() for t in (kc, ks, vc, vs)], (pages, ps, hk, 2 * half)
+    return ptrs, (pages, ps, hk, 2 * half)
 
 
 def qknorm_rope_append_kv4(q_in, k_in: torch.Tensor, v_in: torch.Tensor, gamma_q, gamma_k, cos_sin: torch.Tensor,
@@ -266,12 +299,17 @@ def qknorm_rope_append_kv4(q_in, k_in: torch.Tensor, v_in: torch.Tensor, gamma_q
                                       interleaved, stream)
     if hk != heads:
         raise ValueError(f"k_in has {hk} heads, the cache {heads}")
-    s = _ints(slots, "slots", T, torch.int64, dev)
+    s = _flat(slots, "slots", T, torch.int64, dev)
     with _on(dev):
-        st = capi().qknorm_rope_append_kv4(*args, *ptrs, pages, ps, s, float(eps), _DTYPES[k_in.dtype],
+        st = capi().qknorm_rope_append_kv4(*args, *ptrs, pages, ps, s, eps, _DTYPES[k_in.dtype],
                                            _stream_handle(stream, dev))
     _clib.check(st, "qknorm_rope_append_kv4")
     return q_out
+
+
+class _Of(NamedTuple):
+    device: torch.device
+    dtype: torch.dtype
 
 
 def qknorm_kv4_read(cache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16, *, k_out=None, v_out=None,
@@ -283,18 +321,20 @@ def qknorm_kv4_read(cache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloa
     if dtype not in (torch.float32, torch.bfloat16, torch.float16):
         raise TypeError(f"dtype {dtype} unsupported (float32, bfloat16, float16)")
     n = slots.numel()
-    s = _ints(slots, "slots", n, torch.int64, dev)
-    fresh = []
+    s = _flat(slots, "slots", n, torch.int64, dev)
+    W = hk * d
+    made = []
     if k_out is None:
-        fresh.append(k_out := torch.empty((n, hk * d), dtype=dtype, device=dev))
+        made.append(k_out := torch.empty((n, W), dtype=dtype, device=dev))
+        sk = W
+    else:
+        sk = _match(k_out, "k_out", _Of(dev, dtype), n, W)
     if v_out is None:
-        fresh.append(v_out := torch.empty((n, hk * d), dtype=dtype, device=dev))
-    _used_on(stream, *fresh)
-    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        _same(dev, dtype, t, name)
-    (Tk, Wk, sk), (Tv, Wv, sv) = _rows(k_out, "k_out"), _rows(v_out, "v_out")
-    if (Tk, Wk) != (n, hk * d) or (Tv, Wv) != (n, hk * d):
-        raise ValueError(f"k_out and v_out must be [{n}, {hk * d}]")
+        made.append(v_out := k_out.new_empty((n, W)))
+        sv = W
+    else:
+        sv = _match(v_out, "v_out", _Of(dev, dtype), n, W)
+    _used_on(stream, *made)
     with _on(dev):
         st = capi().qknorm_kv4_read(*ptrs, pages, ps, hk, d, s, n, k_out.data_ptr(), sk, v_out.data_ptr(), sv,
                                     _DTYPES[dtype], _stream_handle(stream, dev))
@@ -327,29 +367,41 @@ def qknorm_kv4_attention(q: torch.Tensor, cache, block_table: torch.Tensor, seq_
     dev, dt = q.device, q.dtype
     ptrs, (pages, ps, hk, d) = _kv4_args(cache, dev)
     hq = _heads(W, d, "q")
-    if not (isinstance(block_table, torch.Tensor) and block_table.dim() == 2):
+    if not isinstance(block_table, torch.Tensor) or len(block_table.shape) != 2:
         raise ValueError("block_table must be [B, max_pages]")
     B, max_pages = block_table.shape
-    bt = _ints(block_table, "block_table", B * max_pages, torch.int32, dev)
-    sl = _ints(seq_lens, "seq_lens", B, torch.int32, dev)
-    qs = None if q_start is None else _ints(q_start, "q_start", B + 1, torch.int32, dev)
-    fresh = []
+    i32 = torch.int32
+    bt = _flat(block_table, "block_table", B * max_pages, i32, dev)
+    sl = _flat(seq_lens, "seq_lens", B, i32, dev)
+    qs = None if q_start is None else _flat(q_start, "q_start", B + 1, i32, dev)
+    made = []
     if out is None:
-        fresh.append(out := torch.empty((T, W), dtype=dt, device=dev))
-    so = _rows_like(out, "out", q, (T, W))
-    if lse is None and return_lse:
-        fresh.append(lse := torch.empty((T, hq), dtype=torch.float32, device=dev))
-    lp = None if lse is None else _vec(lse, "lse", T * hq, torch.float32, dev)
-    need = capi().qknorm_kv4_attention_workspace_bytes(T, B, hq, hk, d, int(max_q_len), int(max_seq_len))
+        made.append(out := q.new_empty((T, W)))
+        so = W
+    else:
+        so = _match(out, "out", q, T, W)
+    if lse is not None:
+        lp = _flat(lse, "lse", T * hq, torch.float32, dev)
+    elif return_lse:
+        made.append(lse := torch.empty((T, hq), dtype=torch.float32, device=dev))
+        lp = lse.data_ptr()
+    else:
+        lp = None
+    lib = capi()
     if workspace is None:
-        fresh.append(workspace := _workspace(None, need, dev))
-    workspace = _workspace(workspace, need, dev)
-    _used_on(stream, *fresh)
-    scale = 1.0 / math.sqrt(d) if softmax_scale is None else float(softmax_scale)
+        need = lib.qknorm_kv4_attention_workspace_bytes(T, B, hq, hk, d, max_q_len, max_seq_len)
+        if need > 0:
+            made.append(workspace := block_table.new_empty((need // 4,)))
+            ws, ws_bytes = workspace.data_ptr(), need
+        else:
+            ws, ws_bytes = None, 0
+    else:
+        ws, ws_bytes = _workspace(workspace, dev)
+    _used_on(stream, *made)
+    scale = 1.0 / math.sqrt(d) if softmax_scale is None else softmax_scale
     with _on(dev):
-        st = capi().qknorm_kv4_attention(q.data_ptr(), sq, out.data_ptr(), so, lp, hq, *ptrs, pages, ps, hk, d, bt,
-                                         max_pages, sl, qs, T, B, int(max_q_len), int(max_seq_len), int(window), scale,
-                                         workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                         _DTYPES[dt], _stream_handle(stream, dev))
+        st = lib.qknorm_kv4_attention(q.data_ptr(), sq, out.data_ptr(), so, lp, hq, *ptrs, pages, ps, hk, d, bt,
+                                      max_pages, sl, qs, T, B, max_q_len, max_seq_len, window, scale, ws, ws_bytes,
+                                      _DTYPES[dt], _stream_handle(stream, dev))
     _clib.check(st, "qknorm_kv4_attention")
     return (out, lse) if return_lse else out
