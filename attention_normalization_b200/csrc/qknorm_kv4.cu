@@ -120,12 +120,14 @@ __device__ __forceinline__ float finish_lse(float m, float total) {  // base 2 -
 // p * (value scale), not p alone, and by an offset of 2^7.  The row sum l takes
 // the unrounded weights.
 //
-// The reference exponent moves only when a scaled weight would exceed 2^15 (one
-// vote per tile); the exact maximum is not needed, as l and O share it.
+// The reference exponent moves only when a scaled weight would exceed 2^15, or a
+// weight 2^75 where the values are (nearly) zeros: one vote per step.  The exact
+// maximum is not needed, as l and O share the reference.
 constexpr int kAttnWarps = 4;
 constexpr int kLeastShare = 32;  // tiles: 8 for each warp
 // What beginning and ending a unit costs a CTA, in tiles: shares are equal in
-// tiles and units alike (a batch of 64 sequences of 1024 to 4096 tokens: 63.4 us without, 60.3 with).
+// tiles and units alike (64 sequences of 1024 to 4096 tokens, 8 KV heads: 63.4 us
+// without this, 60.3 us with it).
 constexpr int kUnitCost = 16;
 constexpr float kOffset = 7.0f, kLargest = 32768.0f;
 
@@ -444,6 +446,7 @@ __device__ __forceinline__ void attend_unit(const Kv4AttnParams &p, const Seq &s
                     w[e] = hide >> e & 1u ? 0.0f : ex2(fmaf(s[h][j][e], qmul[j][e & 1], ref[j][e & 1]));
                 grown[h][j][0] = w[0] + w[2];
                 grown[h][j][1] = w[1] + w[3];
+                big = fmaxf(big, fmaxf(grown[h][j][0], grown[h][j][1]) * 8.6736174e-19f);  // 2^-60: where the values are zeros
 #pragma unroll
                 for (int gr = 0; gr < G; ++gr) {
                     float x[4];

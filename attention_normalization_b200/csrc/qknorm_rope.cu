@@ -651,147 +651,180 @@ constexpr int kManyHeads = 2;
 // CTAs of an SM that the registers are kept low enough for: what the loads of
 // so short-lived warps need to overlap.
 template <typename E, int SINK>
-constexpr int kVectorResident = SINK == kSinkKv4 ? 5 : sizeof(typename Elem<E>::Bits) == 1 ? 4 : 7;
+constexpr int kVectorResident = SINK == kSinkKv4 ? 6 : sizeof(typename Elem<E>::Bits) == 1 ? 4 : 7;
+
+// What a warp of the vector kernels works on: heads [first, end) of token t of
+// one tensor, this lane's head of the first lot h.
+struct WarpHeads {
+    int64_t t;
+    int which, first, end, h;
+};
+__device__ __forceinline__ bool warp_heads(const RopeParams &p, int lanes, WarpHeads &w) {
+    const uint32_t item = blockIdx.x * kVectorWarps + (threadIdx.x >> 5);
+    const uint32_t t32 = item / static_cast<uint32_t>(p.chunks);
+    w.t = t32;
+    if (w.t >= p.T) return false;
+    int chunk = static_cast<int>(item - t32 * p.chunks);
+    w.which = 0;  // Q's chunks, then K's, then V's
+    if (chunk >= p.chunks_of[0]) {
+        chunk -= p.chunks_of[0];
+        w.which = 1;
+        if (chunk >= p.chunks_of[1]) {
+            chunk -= p.chunks_of[1];
+            w.which = 2;
+        }
+    }
+    const int heads = w.which == 0 ? p.chunk_heads : p.chunk_kv_heads;
+    w.first = chunk * heads;
+    w.end = min(p.heads[w.which], w.first + heads);
+    w.h = w.first + (threadIdx.x & 31) / lanes;
+    return true;
+}
+
+// K's or V's heads into the 4-bit cache, the next heads' loads ahead of the work
+// on those at hand.
+template <typename E, int L>
+__device__ __forceinline__ void heads_to_kv4(const RopeParams &p, const WarpHeads &w) {
+    constexpr int V = Elem<E>::kPerVec, kEsz = sizeof(typename Elem<E>::Bits), per = 32 / L;
+    const int u = threadIdx.x & (L - 1);
+    const LanePlace<E> at = lane_place<E>(p, u);
+    const int head_bytes = p.head_dim * kEsz;
+    const char *in = p.in[w.which] + w.t * p.stride[w.which] + w.h * head_bytes;
+    const int64_t slot = p.slots[w.t];
+    if (slot < 0 || slot >= p.num_slots) return;
+    uint4 va = make_uint4(0, 0, 0, 0), vb = va, na = va, nb = va;
+    if (w.h < w.end) {
+        va = ld_stream(in + at.lo * kEsz);
+        vb = ld_stream(in + at.hi * kEsz);
+    }
+    const int64_t page = slot / p.page_size, off = slot - page * p.page_size;
+    const int kv = w.which - 1;
+    int turn = kTurnRow;
+    PairFactors<V / 2> f;
+    if (kv == 0) {
+        const int64_t pos = p.positions[w.t];
+        turn = turn_of(pos, p.table_rows);
+        if (turn == kTurnRow) f = pair_factors<E>(p, at, p.gamma[1], p.table + pos * 2 * p.half);
+    }
+#pragma unroll 1
+    for (int from = 0; w.first + from < w.end; from += per, va = na, vb = nb) {
+        if (w.h + from + per < w.end) {
+            na = ld_stream(in + (from + per) * head_bytes + at.lo * kEsz);
+            nb = ld_stream(in + (from + per) * head_bytes + at.hi * kEsz);
+        }
+        const bool there = w.h + from < w.end;
+        uint32_t unsure = 0xFFFFFFFFu;
+        if (turn == kTurnRow) {
+            if (p.interleaved) part_pairs<E>(va, vb);
+            F2 a[V / 2], b[V / 2];
+            if (kv == 0) {
+                lane_forward<E, L>(p, at, p.gamma[1] != nullptr, f, va, vb, a, b);
+            } else {
+                Elem<E>::widen(va, a);
+                Elem<E>::widen(vb, b);
+            }
+            const int64_t cell = (page * p.heads[1] + w.h + from) * p.page_size + off;
+            unsure = lane_quantise<E, L>(p, kv == 0, u, there, at, a, b,
+                                         reinterpret_cast<uint8_t *>(p.cache[kv]) + cell * (p.head_dim / 2),
+                                         p.scales[kv] + cell * (p.head_dim / kKv4Group));
+        }
+        if (unsure) {
+            __shared__ double exact[kVectorWarps][L * 2 * V];
+            for (int k = 0; k < per; ++k) {
+                const int head = w.first + from + k;
+                if (head >= w.end || !(unsure >> (k * L) & (L == 32 ? 0xFFFFFFFFu : (1u << L) - 1u))) continue;
+                const int64_t cell = (page * p.heads[1] + head) * p.page_size + off;
+                quantise_head<E>(p, w.which, w.t, p.in[w.which] + w.t * p.stride[w.which] + head * head_bytes,
+                                 exact[threadIdx.x >> 5], reinterpret_cast<uint8_t *>(p.cache[kv]) + cell * (p.head_dim / 2),
+                                 p.scales[kv] + cell * (p.head_dim / kKv4Group));
+            }
+        }
+    }
+}
 
 template <typename E, int SINK, int L>
 __global__ void __launch_bounds__(kVectorWarps * 32, kVectorResident<E, SINK>) heads_vector_kernel(const __grid_constant__ RopeParams p) {
     constexpr int V = Elem<E>::kPerVec;
     constexpr int kEsz = sizeof(typename Elem<E>::Bits);
-    constexpr bool kStay = SINK == kSinkKv4;  // whether a warp goes on to further heads
-    constexpr int U = kStay ? 1 : kManyHeads;  // heads of a lane group loaded at a time
+    constexpr int U = kManyHeads;
     pdl_wait_and_release();
-    const uint32_t item = blockIdx.x * kVectorWarps + (threadIdx.x >> 5);
-    const uint32_t t32 = item / static_cast<uint32_t>(p.chunks);
-    const int64_t t = t32;
-    if (t >= p.T) return;
-    int chunk = static_cast<int>(item - t32 * p.chunks);
     const int lanes = L > 0 ? L : p.lanes;
-    const int lane = threadIdx.x & 31, u = lane & (lanes - 1), per = 32 / lanes;
-    // which tensor: Q's chunks, then K's, then V's
-    int which = 0;
-    if (chunk >= p.chunks_of[0]) {
-        chunk -= p.chunks_of[0];
-        which = 1;
-        if (chunk >= p.chunks_of[1]) {
-            chunk -= p.chunks_of[1];
-            which = 2;
+    const int u = threadIdx.x & (lanes - 1), per = 32 / lanes;
+    WarpHeads w;
+    if (!warp_heads(p, lanes, w)) return;
+    if constexpr (SINK == kSinkKv4) {
+        if (w.which > 0) {
+            heads_to_kv4<E, L>(p, w);
+            return;
         }
     }
-    const int first = chunk * p.chunk_heads, end = min(p.heads[which], first + p.chunk_heads);
-    const int h = first + lane / lanes;
+    const int which = w.which;
     const bool active = L > 0 || u < p.units;
     const LanePlace<E> at = lane_place<E>(p, active ? u : 0);
     const int head_bytes = p.head_dim * kEsz;
-    const char *in = p.in[which] + t * p.stride[which] + h * head_bytes;
-    uint4 va[U], vb[U], na[U], nb[U];  // the heads at hand, the next ones (kStay)
-    auto load = [&](uint4 (&a)[U], uint4 (&b)[U], int from) {  // heads from + j per, counted from h
+    const char *in = p.in[which] + w.t * p.stride[which] + w.h * head_bytes;
+    uint4 va[U], vb[U];
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            a[j] = b[j] = make_uint4(0, 0, 0, 0);
-            if (active && h + from + j * per < end) {
-                a[j] = ld_stream(in + (from + j * per) * head_bytes + at.lo * kEsz);
-                b[j] = ld_stream(in + (from + j * per) * head_bytes + at.hi * kEsz);
-            }
+    for (int j = 0; j < U; ++j) {
+        va[j] = vb[j] = make_uint4(0, 0, 0, 0);
+        if (active && w.h + j * per < w.end) {
+            va[j] = ld_stream(in + j * per * head_bytes + at.lo * kEsz);
+            vb[j] = ld_stream(in + j * per * head_bytes + at.hi * kEsz);
         }
-    };
-    load(va, vb, 0);
-    const int64_t pos = p.positions[t];
-    int64_t page = 0, off = 0;
-    if (SINK != kSinkRows && which > 0) {
-        const int64_t slot = p.slots[t];
-        if (slot < 0 || slot >= p.num_slots) return;
-        page = slot / p.page_size;
-        off = slot - page * p.page_size;
     }
-    char *out = nullptr;
+    const int64_t pos = p.positions[w.t];
+    char *out;
     int64_t step = head_bytes;
-    if (SINK == kSinkRows || which == 0) {
-        out = p.out[which] + t * p.stride[which] + h * step;
-    } else if (SINK == kSinkCache) {
+    if (SINK == kSinkCache && which > 0) {
+        const int64_t slot = p.slots[w.t];
+        if (slot < 0 || slot >= p.num_slots) return;
+        const int64_t page = slot / p.page_size, off = slot - page * p.page_size;
         step = p.head_stride[which - 1];
-        out = p.cache[which - 1] + page * p.page_stride[which - 1] + off * p.token_stride[which - 1] + h * step;
+        out = p.cache[which - 1] + page * p.page_stride[which - 1] + off * p.token_stride[which - 1] + w.h * step;
+        if (which == 2) {  // values as they are
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                if (active && w.h + j * per < w.end) {
+                    *reinterpret_cast<uint4 *>(out + j * per * step + at.lo * kEsz) = va[j];
+                    *reinterpret_cast<uint4 *>(out + j * per * step + at.hi * kEsz) = vb[j];
+                }
+            }
+            return;
+        }
+    } else {
+        out = p.out[which] + w.t * p.stride[which] + w.h * step;
     }
-    const int turn = which == 2 ? static_cast<int>(kTurnRow) : turn_of(pos, p.table_rows);
-    const float *cs = p.table + (turn == kTurnRow && which < 2 ? pos * 2 * p.half : 0);
-    if (turn != kTurnRow && (SINK != kSinkKv4 || which == 0)) {  // zeros or NaN for all of the token's heads
+    const int turn = turn_of(pos, p.table_rows);
+    if (turn != kTurnRow) {  // zeros or NaN for all of the token's heads
         F2 x[V / 2];
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) {
             const float v = turn == kTurnPad ? 0.0f : __uint_as_float(0x7FFFFFFFu);
             x[i] = f2(v, v);
         }
-        const uint4 w = Elem<E>::narrow(x);
-        for (int from = 0; active && h + from < end; from += per) {
-            const int64_t o = static_cast<int64_t>(from) * step;
-            st_stream(out + o + at.lo * kEsz, w);
-            st_stream(out + o + at.hi * kEsz, w);
+        const uint4 fill = Elem<E>::narrow(x);
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            if (active && w.h + j * per < w.end) {
+                st_stream(out + j * per * step + at.lo * kEsz, fill);
+                st_stream(out + j * per * step + at.hi * kEsz, fill);
+            }
         }
         return;
     }
-    const char *gamma = which < 2 ? p.gamma[which] : nullptr;
-    PairFactors<V / 2> f;
-    if (which < 2 && turn == kTurnRow) f = pair_factors<E>(p, at, gamma, cs);
-#pragma unroll 1
-    for (int from = 0; first + from < end; from += U * per) {
-        if (kStay && first + from + U * per < end) load(na, nb, from + U * per);
+    const char *gamma = p.gamma[which];
+    const PairFactors<V / 2> f = pair_factors<E>(p, at, gamma, p.table + pos * 2 * p.half);
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const int here = from + j * per;
-            const bool there = active && h + here < end;
-            const int64_t o = static_cast<int64_t>(here) * step;
-            if (SINK == kSinkCache && which == 2) {  // values as they are
-                if (there) {
-                    *reinterpret_cast<uint4 *>(out + o + at.lo * kEsz) = va[j];
-                    *reinterpret_cast<uint4 *>(out + o + at.hi * kEsz) = vb[j];
-                }
-                continue;
-            }
-            if (p.interleaved) part_pairs<E>(va[j], vb[j]);
-            F2 a[V / 2], b[V / 2];
-            if constexpr (SINK == kSinkKv4) {
-                if (which > 0) {
-                    const int kv = which - 1;
-                    const int64_t cell = (page * p.heads[1] + h + here) * p.page_size + off;
-                    uint8_t *codes = reinterpret_cast<uint8_t *>(p.cache[kv]) + cell * (p.head_dim / 2);
-                    __half *scales = p.scales[kv] + cell * (p.head_dim / kKv4Group);
-                    uint32_t unsure = 0xFFFFFFFFu;
-                    if (turn == kTurnRow) {
-                        if (kv == 0) {
-                            lane_forward<E, L>(p, at, gamma != nullptr, f, va[j], vb[j], a, b);
-                        } else {
-                            Elem<E>::widen(va[j], a);
-                            Elem<E>::widen(vb[j], b);
-                        }
-                        unsure = lane_quantise<E, L>(p, kv == 0, u, there, at, a, b, codes, scales);
-                    }
-                    if (unsure) {
-                        __shared__ double exact[kVectorWarps][L * 2 * V];
-                        for (int k = 0; k < 32 / L; ++k) {
-                            const int head = first + here + k;
-                            if (head >= end || !(unsure >> (k * L) & (L == 32 ? 0xFFFFFFFFu : (1u << L) - 1u))) continue;
-                            const int64_t at_cell = (page * p.heads[1] + head) * p.page_size + off;
-                            quantise_head<E>(p, which, t, p.in[which] + t * p.stride[which] + head * head_bytes,
-                                             exact[threadIdx.x >> 5],
-                                             reinterpret_cast<uint8_t *>(p.cache[kv]) + at_cell * (p.head_dim / 2),
-                                             p.scales[kv] + at_cell * (p.head_dim / kKv4Group));
-                        }
-                    }
-                    continue;
-                }
-            }
-            lane_forward<E, L>(p, at, gamma != nullptr, f, va[j], vb[j], a, b);
-            uint4 wa = Elem<E>::narrow(a), wb = Elem<E>::narrow(b);
-            if (p.interleaved) join_pairs<E>(wa, wb);
-            if (there) {
-                st_stream(out + o + at.lo * kEsz, wa);
-                st_stream(out + o + at.hi * kEsz, wb);
-            }
-        }
-        if constexpr (kStay) {
-#pragma unroll
-            for (int j = 0; j < U; ++j) va[j] = na[j], vb[j] = nb[j];
-        } else {
-            break;
+    for (int j = 0; j < U; ++j) {
+        if (w.first + j * per >= w.end) break;
+        if (p.interleaved) part_pairs<E>(va[j], vb[j]);
+        F2 a[V / 2], b[V / 2];
+        lane_forward<E, L>(p, at, gamma != nullptr, f, va[j], vb[j], a, b);
+        uint4 wa = Elem<E>::narrow(a), wb = Elem<E>::narrow(b);
+        if (p.interleaved) join_pairs<E>(wa, wb);
+        if (active && w.h + j * per < w.end) {
+            st_stream(out + j * per * step + at.lo * kEsz, wa);
+            st_stream(out + j * per * step + at.hi * kEsz, wb);
         }
     }
 }
@@ -1109,9 +1142,14 @@ qkn_status launch_heads(RopeParams &p, int dtype, bool aligned, void *stream) {
     p.lanes = aligned ? vector_lanes(dtype, p.head_dim, p.half) : 0;
     if (p.lanes > 0) {
         p.units = p.head_dim / (2 * (16 / elem_bytes(dtype)));
-        p.chunk_heads = (32 / p.lanes) * head_groups(rows, 32 / p.lanes, sms, SINK == kSinkKv4 ? 4 : kManyHeads);
+        const int per = 32 / p.lanes;
+        p.chunk_heads = per * head_groups(rows, per, sms, kManyHeads);
+        p.chunk_kv_heads = SINK == kSinkKv4 ? per * head_groups(rows, per, sms, 4) : p.chunk_heads;
         p.chunks = 0;
-        for (int i = 0; i < 3; ++i) p.chunks += p.chunks_of[i] = (p.heads[i] + p.chunk_heads - 1) / p.chunk_heads;
+        for (int i = 0; i < 3; ++i) {
+            const int heads = i ? p.chunk_kv_heads : p.chunk_heads;
+            p.chunks += p.chunks_of[i] = (p.heads[i] + heads - 1) / heads;
+        }
         const int64_t ctas = (p.T * p.chunks + kVectorWarps - 1) / kVectorWarps;
         return launched(launch_pdl(vector_kernel<SINK>(dtype, p.lanes, p.lanes == p.units), dim3((unsigned)ctas),
                                    kVectorWarps * 32, 0, stream, p));

@@ -37,7 +37,8 @@ struct RopeParams {
     int32_t lanes;               // vector kernel: units rounded up to a power of two
     int32_t chunks;              // vector kernel: warps per token,
     int32_t chunks_of[3];        // of which each tensor's,
-    int32_t chunk_heads;         // and the heads of a warp
+    int32_t chunk_heads;         // and the heads of a warp: Q's,
+    int32_t chunk_kv_heads;      // K's and V's
     float eps;
     float inv_d;                 // 1 / head_dim
     // caches (kSinkCache: bytes; kSinkKv4: codes, then scales)

@@ -259,8 +259,8 @@ qkn_status qknorm_headwise(const void *q_in, void *q_out, const void *gamma_q, i
  * runs.
  * Errors: as qknorm_headwise, plus QKN_ERR_INVALID_ARG for an odd rotary_dim
  * or one outside [0, head_dim], null or unaligned positions or cos_sin, an
- * output overlapping them, or T * heads >= 2^31; QKN_ERR_UNSUPPORTED for
- * head_dim > 1024.  (No paper counterpart: the page stops at the norm.)
+ * output overlapping them, more than 65536 heads, or T * heads >= 2^31;
+ * QKN_ERR_UNSUPPORTED for head_dim > 1024.  (No paper counterpart: the page stops at the norm.)
  */
 qkn_status qknorm_headwise_rope(const void *q_in, void *q_out, const void *gamma_q, int64_t q_stride, int32_t q_heads,
                                 const void *k_in, void *k_out, const void *gamma_k, int64_t k_stride, int32_t k_heads,
@@ -341,8 +341,8 @@ qkn_status qknorm_rope_append(const void *q_in, void *q_out, const void *gamma_q
  * stands for c_j * s.  Codes and scales are the correctly rounded ones of the
  * formula in 64 bits, so they do not depend on the kernel variant.  A group
  * with a NaN or an infinity gets a NaN scale and reads as NaN.
- * head_dim is 64, 128 or 256 and page_size a multiple of 16 (else
- * QKN_ERR_UNSUPPORTED).
+ * head_dim is 64, 128 or 256, page_size a multiple of 16 and a page's codes
+ * below 2 GiB (else QKN_ERR_UNSUPPORTED).
  *
  * qknorm_rope_append_kv4 is qknorm_rope_append into it (float32, bfloat16 or
  * float16 rows).  qknorm_kv4_read gives n cached tokens back as K and V rows

@@ -532,6 +532,108 @@ def test_attention_over_a_long_cache(hq, hk, D, L, window):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("hq,hk,D,dtype,rows,window", [(8, 4, 128, BF16, 1, 0), (16, 2, 64, F16, 3, 0), (6, 3, 256, BF16, 2, 700)])
+def test_attention_of_many_uneven_sequences(hq, hk, D, dtype, rows, window):
+    """Enough tokens to be cut into shares, which then begin and end inside
+    sequences, in ones without tokens and in ones without rows."""
+    g = torch.Generator().manual_seed(D + rows)
+    ps, B = 32, 23
+    lens = [int(x) for x in torch.randint(0, 1500, (B,), generator=g)]
+    lens[0], lens[5], lens[6], lens[22] = 2900, 0, 1, 0
+    qn = [rows] * B
+    if rows > 1:
+        qn[3] = qn[22] = 0
+        qn[7] = 1
+    pages = sum(-(-n // ps) for n in lens)
+    cache = random_cache(pages, ps, hk, D, g)
+    q_start = torch.tensor([0, *np.cumsum(qn)], dtype=torch.int32)
+    q = torch.randn((int(q_start[-1]) + 1, hq * D), generator=g).to(dtype).to(DEV)
+    check_attention(q, cache, tables(lens, ps, pages, g), torch.tensor(lens, dtype=torch.int32),
+                    None if rows == 1 else q_start, rows, 3000, window)
+
+
+@pytest.mark.gpu
+def test_attention_to_a_token_whose_values_are_zeros():
+    """All weight on a token with zero values, hundreds of powers of two above
+    the others, wherever it comes: zeros, and its score as lse."""
+    g = torch.Generator().manual_seed(12)
+    hq, hk, D, ps, L = 4, 1, 128, 16, 1100
+    for zero in (0, 40, 700, L - 1):
+        cache = random_cache(70, ps, hk, D, g)
+        bt = torch.arange(70, dtype=torch.int32).view(1, 70)
+        q = torch.randn((1, hq * D), generator=g).to(BF16).to(DEV)
+        page, off = zero // ps, zero % ps
+        cache[1][page, 0, off] = 200.0
+        # codes of the query's signs: a large positive score for head 0
+        sign = (q[0, :D].float() >= 0).cpu()
+        c = torch.where(sign, 15, 1).to(torch.uint8)
+        cache[0][page, 0, off] = (c[0::2] | (c[1::2] << 4)).to(DEV)
+        cache[2][page, 0, off] = 0x88
+        cache[3][page, 0, off] = 0.0
+        out, lse = check_attention(q, cache, bt, torch.tensor([L], dtype=torch.int32), None, 1, L)
+        assert not out[0, :D].any() and float(lse[0, 0]) > 1000
+
+
+@pytest.mark.gpu
+def test_caches_past_four_gigabytes():
+    """The last cells of caches whose offsets do not fit 32 bits."""
+    g = torch.Generator().manual_seed(13)
+    hq, hk, D, ps = 8, 8, 256, 16
+    T, pages = 3, 70000  # 4.6 GB of bfloat16 each
+    x = torch.randn((T, (hq + 2 * hk) * D), generator=g).to(BF16).to(DEV)
+    q, k, v = x[:, :hq * D], x[:, hq * D:(hq + hk) * D], x[:, (hq + hk) * D:]
+    gm, cs, pos = gamma_of(D, BF16, g), table(8, D), torch.tensor([1, 2, 3])
+    slots = torch.tensor([pages * ps - 1, 5, (pages - 2) * ps + 3])
+    kc, vc = (torch.empty((pages, ps, hk, D), dtype=BF16, device=DEV) for _ in range(2))
+    qk.qknorm_rope_append(q, k, v, gm.to(DEV), gm.to(DEV), D, cs.to(DEV), pos.to(DEV), kc, vc, slots.to(DEV), EPS)
+    y, mag = forward(k, gm, D, cs, pos, False)
+    at = (slots.to(DEV) // ps, slots.to(DEV) % ps)
+    check(kc[at], y, mag, BF16)
+    assert torch.equal(vc[at].reshape(T, -1), v)
+    del kc, vc
+    pages = 270000  # 4.4 GB of codes each
+    cache = tuple(torch.empty(s, dtype=t, device=DEV) for _ in range(2) for s, t in (
+        ((pages, hk, ps, D // 2), torch.uint8), ((pages, hk, ps, D // 64), torch.float16)))
+    slots = torch.arange(T) + (pages - 1) * ps
+    q_out = qk.qknorm_rope_append_kv4(q, k, v, gm.to(DEV), gm.to(DEV), cs.to(DEV), pos.to(DEV), cache, slots.to(DEV), EPS)
+    kr, vr = qk.qknorm_kv4_read(cache, slots.to(DEV), F32)
+    for got, want in ((kr, y), (vr, f64(v).reshape(T, hk, D))):
+        c, s = quantise(want.numpy())
+        value = (torch.from_numpy(c).double() - 8) * torch.from_numpy(s).double().repeat_interleave(64, -1)
+        assert torch.equal(got.cpu().double(), value.reshape(T, -1))
+    small = tuple(t[-1:].clone() for t in cache)
+    lens, one = torch.tensor([T], dtype=torch.int32, device=DEV), torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    outs = [qk.qknorm_kv4_attention(q_out, c, torch.tensor([[p]], dtype=torch.int32, device=DEV), lens, max_seq_len=16,
+                                    q_start=one, max_q_len=T) for c, p in ((cache, pages - 1), (small, 0))]
+    assert torch.equal(*outs)
+
+
+@pytest.mark.gpu
+def test_calls_at_once_on_two_streams():
+    """Two long attentions and a gradient on streams of their own, their
+    workspaces made for each call, equal to the same calls alone."""
+    g = torch.Generator().manual_seed(14)
+    hq, hk, D, ps, L = 8, 2, 128, 64, 9000
+    pages = -(-L // ps)
+    bt, lens = torch.arange(pages, dtype=torch.int32, device=DEV).view(1, -1), torch.tensor([L], dtype=torch.int32, device=DEV)
+    caches = [random_cache(pages, ps, hk, D, g) for _ in range(2)]
+    qs = [torch.randn((1, hq * D), generator=g).to(BF16).to(DEV) for _ in range(2)]
+    x, dy = (torch.randn((700, hq * D), generator=g).to(BF16).to(DEV) for _ in range(2))
+    gm, cs, pos = gamma_of(D, BF16, g).to(DEV), table(700, D).to(DEV), torch.arange(700, device=DEV)
+
+    def calls(streams):
+        out = [qk.qknorm_kv4_attention(q, c, bt, lens, max_seq_len=L, stream=s) for q, c, s in zip(qs, caches, streams)]
+        return [*out, *qk.qknorm_headwise_rope_backward(dy, dy, x, x, gm, gm, D, cs, pos, stream=streams[2])]
+    alone = calls([None] * 3)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        streams = [torch.cuda.Stream() for _ in range(3)]
+        for a, b in zip(calls(streams), alone):
+            torch.cuda.synchronize()
+            assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
 def test_attention_ignores_what_is_masked_and_missing():
     """NaN and infinite scales behind the length, before the window and on pages
     that are not in the table; page numbers outside the cache count as absent."""
