@@ -18,30 +18,52 @@ from typing import NamedTuple
 
 import torch
 
-from . import _DTYPES, _clib, _on, _rows, _same, _stream_handle, capi, gamma_dtype
+from . import _DTYPES, _clib, _on, _raw_current_stream, _rows, _stream_handle, capi, gamma_dtype
 
-# These calls are short on the GPU, so their checks are kept few and flat: each
-# operand is looked at once, and what is made here is not looked at again.
+# These calls are short on the GPU, so what they look at on the host is kept
+# small: each operand once, its device as a number, what is made here not at all.
+
+_Tensor = torch.Tensor
+_GAMMA = {dt: gamma_dtype(dt) for dt in _DTYPES}
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _like(t, name, dev, dt):
-    """(T, width, row stride) of the rows `t`, on `dev` and of type `dt`."""
-    if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype != dt:
-        _rows(t, name)
-        _same(dev, dt, t, name)
-    shape, stride = t.shape, t.stride()
+def _call(fn, where, index, stream, *args):
+    """`fn(*args, stream)` with device `index` current."""
+    if stream is None and _raw_current_stream is not None and index == _current_device():
+        st = fn(*args, _raw_current_stream(index))
+    else:
+        dev = torch.device("cuda", index)
+        with _on(dev):
+            st = fn(*args, _stream_handle(stream, dev))
+    if st:
+        _clib.check(st, where)
+
+
+def _first(t, name):
+    """(T, width, row stride, device number, type) of the rows that the call's
+    other operands have to go with."""
+    T, W, s = _rows(t, name)
+    return T, W, s, t.get_device(), t.dtype
+
+
+def _like(t, name, index, dt):
+    """(T, width, row stride) of the rows `t`, on device `index` and of type `dt`."""
+    if not isinstance(t, _Tensor) or t.dtype is not dt or t.get_device() != index:
+        raise ValueError(f"{name} must be a tensor on cuda:{index} with dtype {dt}")
+    shape = t.shape
     if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D [T, width]")
     T, W = shape
-    if stride[1] != 1 and T > 0 and W > 1:
+    s0, s1 = t.stride()
+    if s1 != 1 and T > 0 and W > 1:
         raise ValueError(f"{name} rows must be unit-stride along the width")
-    return T, W, (stride[0] if T > 1 else max(stride[0], W))
+    return T, W, (s0 if T > 1 else max(s0, W))
 
 
-def _match(t, name, like, T, W, stride=None):
-    """Row stride of the [T, W] rows `t` on the device and of the type of
-    `like`, which has to be `stride` where that is given."""
-    To, Wo, s = _like(t, name, like.device, like.dtype)
+def _match(t, name, index, dt, T, W, stride=None):
+    """Row stride of the [T, W] rows `t`, which has to be `stride` where that is given."""
+    To, Wo, s = _like(t, name, index, dt)
     if To != T or Wo != W:
         raise ValueError(f"{name} must be [{T}, {W}]")
     if stride is not None and s != stride and T > 1:
@@ -49,17 +71,18 @@ def _match(t, name, like, T, W, stride=None):
     return s
 
 
-def _flat(t, name, n, dtype, dev):
+def _flat(t, name, n, dtype, index):
     """Pointer of a contiguous tensor of `n` elements."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of {n} elements on {dev}")
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.get_device() != index or t.numel() != n \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of {n} elements on cuda:{index}")
     return t.data_ptr()
 
 
-def _table(cos_sin, dev):
-    if not isinstance(cos_sin, torch.Tensor) or cos_sin.dtype != torch.float32 or cos_sin.device != dev \
+def _table(cos_sin, index):
+    if not isinstance(cos_sin, _Tensor) or cos_sin.dtype is not torch.float32 or cos_sin.get_device() != index \
             or len(cos_sin.shape) != 2 or not cos_sin.is_contiguous():
-        raise ValueError(f"cos_sin must be a contiguous float32 CUDA tensor [table_rows, rotary_dim] on {dev}")
+        raise ValueError(f"cos_sin must be a contiguous float32 CUDA tensor [table_rows, rotary_dim] on cuda:{index}")
     P, rot = cos_sin.shape
     return cos_sin.data_ptr(), P, rot
 
@@ -84,31 +107,28 @@ def qknorm_headwise_rope(q_in: torch.Tensor, k_in: torch.Tensor, gamma_q: torch.
     """Headwise QK-Norm and position rotation of every Q and K head in one
     launch; returns ``(q_out, k_out)``.  ``interleaved`` rotates the pairs
     ``(2i, 2i + 1)`` instead of ``(i, i + rotary_dim / 2)``."""
-    T, Wq, sq = _rows(q_in, "q_in")
-    dev, dt = q_in.device, q_in.dtype
+    T, Wq, sq, dev, dt = _first(q_in, "q_in")
     Tk, Wk, sk = _like(k_in, "k_in", dev, dt)
     if T != Tk:
         raise ValueError("q_in and k_in must have the same number of tokens")
     table, P, rot = _table(cos_sin, dev)
     pos = _flat(positions, "positions", T, torch.int64, dev)
-    gdt = gamma_dtype(dt)
+    gdt = _GAMMA[dt]
     gq, gk = _flat(gamma_q, "gamma_q", head_dim, gdt, dev), _flat(gamma_k, "gamma_k", head_dim, gdt, dev)
     if q_out is None:
         q_out = q_in.new_empty_strided((T, Wq), (sq, 1))
         _used_on(stream, q_out)
     else:
-        _match(q_out, "q_out", q_in, T, Wq, sq)
+        _match(q_out, "q_out", dev, dt, T, Wq, sq)
     if k_out is None:
         k_out = k_in.new_empty_strided((T, Wk), (sk, 1))
         _used_on(stream, k_out)
     else:
-        _match(k_out, "k_out", k_in, T, Wk, sk)
-    with _on(dev):
-        st = capi().qknorm_headwise_rope(
-            q_in.data_ptr(), q_out.data_ptr(), gq, sq, _heads(Wq, head_dim, "q_in"), k_in.data_ptr(), k_out.data_ptr(),
-            gk, sk, _heads(Wk, head_dim, "k_in"), T, head_dim, table, P, rot, 1 if interleaved else 0, pos, eps,
-            _DTYPES[dt], _stream_handle(stream, dev))
-    _clib.check(st, "qknorm_headwise_rope")
+        _match(k_out, "k_out", dev, dt, T, Wk, sk)
+    _call(capi().qknorm_headwise_rope, "qknorm_headwise_rope", dev, stream,
+          q_in.data_ptr(), q_out.data_ptr(), gq, sq, _heads(Wq, head_dim, "q_in"), k_in.data_ptr(), k_out.data_ptr(),
+          gk, sk, _heads(Wk, head_dim, "k_in"), T, head_dim, table, P, rot, 1 if interleaved else 0, pos, eps,
+          _DTYPES[dt])
     return q_out, k_out
 
 
@@ -122,8 +142,8 @@ def rope_backward_workspace_bytes(T: int, q_heads: int, k_heads: int, head_dim: 
 
 def _workspace(workspace, dev):
     """Pointer and bytes of a caller's workspace."""
-    if not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous CUDA tensor on {dev}")
+    if not isinstance(workspace, _Tensor) or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on cuda:{dev}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -135,28 +155,27 @@ def qknorm_headwise_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q_
     gradients of its outputs, ``q_in`` and ``k_in`` the rows it read.  Returns
     ``(dq_in, dk_in, dgamma_q, dgamma_k)``, the last two fp32 ``[head_dim]``
     summed over tokens and heads (overwritten, not accumulated)."""
-    T, Wq, sq = _rows(q_in, "q_in")
-    dev, dt = q_in.device, q_in.dtype
+    T, Wq, sq, dev, dt = _first(q_in, "q_in")
     Tk, Wk, sk = _like(k_in, "k_in", dev, dt)
     if T != Tk:
         raise ValueError("q_in and k_in must have the same number of tokens")
     hq, hk = _heads(Wq, head_dim, "q_in"), _heads(Wk, head_dim, "k_in")
     table, P, rot = _table(cos_sin, dev)
     pos = _flat(positions, "positions", T, torch.int64, dev)
-    gdt, f32 = gamma_dtype(dt), torch.float32
+    gdt, f32 = _GAMMA[dt], torch.float32
     gq, gk = _flat(gamma_q, "gamma_q", head_dim, gdt, dev), _flat(gamma_k, "gamma_k", head_dim, gdt, dev)
-    dqs, dks = _match(dq_out, "dq_out", q_in, T, Wq), _match(dk_out, "dk_out", k_in, T, Wk)
+    dqs, dks = _match(dq_out, "dq_out", dev, dt, T, Wq), _match(dk_out, "dk_out", dev, dt, T, Wk)
     made = []
     if dq_in is None:
         made.append(dq_in := q_in.new_empty((T, Wq)))
         dqi = Wq
     else:
-        dqi = _match(dq_in, "dq_in", q_in, T, Wq)
+        dqi = _match(dq_in, "dq_in", dev, dt, T, Wq)
     if dk_in is None:
         made.append(dk_in := k_in.new_empty((T, Wk)))
         dki = Wk
     else:
-        dki = _match(dk_in, "dk_in", k_in, T, Wk)
+        dki = _match(dk_in, "dk_in", dev, dt, T, Wk)
     if dgamma_q is None and dgamma_k is None:
         dgamma_q, dgamma_k = made_g = cos_sin.new_empty((2, head_dim)).unbind(0)
         made += made_g
@@ -173,13 +192,10 @@ def qknorm_headwise_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q_
     else:
         ws, ws_bytes = _workspace(workspace, dev)
     _used_on(stream, *made)
-    with _on(dev):
-        st = lib.qknorm_headwise_rope_backward(
-            q_in.data_ptr(), sq, dq_out.data_ptr(), dqs, dq_in.data_ptr(), dqi, gq, pgq, hq,
-            k_in.data_ptr(), sk, dk_out.data_ptr(), dks, dk_in.data_ptr(), dki, gk, pgk, hk,
-            T, head_dim, table, P, rot, 1 if interleaved else 0, pos, eps, ws, ws_bytes, _DTYPES[dt],
-            _stream_handle(stream, dev))
-    _clib.check(st, "qknorm_headwise_rope_backward")
+    _call(lib.qknorm_headwise_rope_backward, "qknorm_headwise_rope_backward", dev, stream,
+          q_in.data_ptr(), sq, dq_out.data_ptr(), dqs, dq_in.data_ptr(), dqi, gq, pgq, hq,
+          k_in.data_ptr(), sk, dk_out.data_ptr(), dks, dk_in.data_ptr(), dki, gk, pgk, hk,
+          T, head_dim, table, P, rot, 1 if interleaved else 0, pos, eps, ws, ws_bytes, _DTYPES[dt])
     return dq_in, dk_in, dgamma_q, dgamma_k
 
 
@@ -189,16 +205,15 @@ _Strides = ctypes.c_int64 * 3
 
 
 def _append_rows(q_in, k_in, v_in, gamma_q, gamma_k, head_dim, cos_sin, positions, q_out, interleaved, stream):
-    """The arguments the two append calls share, the query output and T, kv heads."""
-    T, Wk, sk = _rows(k_in, "k_in")
-    dev, dt = k_in.device, k_in.dtype
-    sv = _match(v_in, "v_in", k_in, T, Wk)
+    """The arguments the two append calls share, the query output, T, kv heads, the device and the type."""
+    T, Wk, sk, dev, dt = _first(k_in, "k_in")
+    sv = _match(v_in, "v_in", dev, dt, T, Wk)
     hk = _heads(Wk, head_dim, "k_in")
     table, P, rot = _table(cos_sin, dev)
     pos = _flat(positions, "positions", T, torch.int64, dev)
     if (gamma_k is None) != (gamma_q is None) and q_in is not None:
         raise ValueError("gamma_q and gamma_k: both (norm and rotation) or neither (rotation only)")
-    gdt = gamma_dtype(dt)
+    gdt = _GAMMA[dt]
     gq = None if gamma_q is None else _flat(gamma_q, "gamma_q", head_dim, gdt, dev)
     gk = None if gamma_k is None else _flat(gamma_k, "gamma_k", head_dim, gdt, dev)
     if q_in is None:
@@ -212,11 +227,11 @@ def _append_rows(q_in, k_in, v_in, gamma_q, gamma_k, head_dim, cos_sin, position
             q_out = q_in.new_empty_strided((T, Wq), (sq, 1))
             _used_on(stream, q_out)
         else:
-            _match(q_out, "q_out", q_in, T, Wq, sq)
+            _match(q_out, "q_out", dev, dt, T, Wq, sq)
         qp, qo = q_in.data_ptr(), q_out.data_ptr()
     args = (qp, qo, gq, sq, hq, k_in.data_ptr(), gk, sk, v_in.data_ptr(), sv, hk, T, head_dim, table, P, rot,
             1 if interleaved else 0, pos)
-    return args, q_out, T, hk
+    return args, q_out, T, hk, dev, dt
 
 
 def qknorm_rope_append(q_in, k_in: torch.Tensor, v_in: torch.Tensor, gamma_q, gamma_k, head_dim: int,
@@ -231,25 +246,22 @@ def qknorm_rope_append(q_in, k_in: torch.Tensor, v_in: torch.Tensor, gamma_q, ga
     place ``slots[t] % page_size``, and nowhere where that lies outside the
     cache.  ``gamma_q`` and ``gamma_k`` of ``None`` leave the norm out, ``q_in``
     of ``None`` the Q rows."""
-    args, q_out, T, hk = _append_rows(q_in, k_in, v_in, gamma_q, gamma_k, head_dim, cos_sin, positions, q_out,
-                                      interleaved, stream)
-    dev = k_in.device
-    dt = k_in.dtype
+    args, q_out, T, hk, dev, dt = _append_rows(q_in, k_in, v_in, gamma_q, gamma_k, head_dim, cos_sin, positions, q_out,
+                                               interleaved, stream)
     pages = k_cache.shape[:2]
     strides = []
     for c, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _same(dev, dt, c, name)
+        if not isinstance(c, _Tensor) or c.dtype is not dt or c.get_device() != dev:
+            raise ValueError(f"{name} must be a tensor on cuda:{dev} with dtype {dt}")
         shape, stride = c.shape, c.stride()
         if len(shape) != 4 or shape[2] != hk or shape[3] != head_dim or (head_dim > 1 and stride[3] != 1):
             raise ValueError(f"{name} must be [pages, page_size, {hk}, {head_dim}] with unit stride along the last")
         if shape[:2] != pages:
             raise ValueError("k_cache and v_cache must have the same pages")
-        strides.append(_Strides(*stride[:3]))
+        strides.append(_Strides(stride[0], stride[1], stride[2]))
     s = _flat(slots, "slots", T, torch.int64, dev)
-    with _on(dev):
-        st = capi().qknorm_rope_append(*args, k_cache.data_ptr(), strides[0], v_cache.data_ptr(), strides[1], *pages, s,
-                                       eps, _DTYPES[dt], _stream_handle(stream, dev))
-    _clib.check(st, "qknorm_rope_append")
+    _call(capi().qknorm_rope_append, "qknorm_rope_append", dev, stream, *args, k_cache.data_ptr(), strides[0],
+          v_cache.data_ptr(), strides[1], *pages, s, eps, _DTYPES[dt])
     return q_out
 
 
@@ -293,52 +305,45 @@ def qknorm_rope_append_kv4(q_in, k_in: torch.Tensor, v_in: torch.Tensor, gamma_q
                            positions: torch.Tensor, cache, slots: torch.Tensor, eps: float = 1e-6, *,
                            interleaved: bool = False, q_out=None, stream=None):
     """``qknorm_rope_append`` into a 4-bit cache (``kv4_cache``); returns ``q_out``."""
-    dev = k_in.device
-    ptrs, (pages, ps, heads, head_dim) = _kv4_args(cache, dev)
-    args, q_out, T, hk = _append_rows(q_in, k_in, v_in, gamma_q, gamma_k, head_dim, cos_sin, positions, q_out,
-                                      interleaved, stream)
+    if not isinstance(k_in, _Tensor) or not k_in.is_cuda:
+        raise ValueError("k_in must be a CUDA tensor (this library has no CPU path)")
+    ptrs, (pages, ps, heads, head_dim) = _kv4_args(cache, k_in.get_device())
+    args, q_out, T, hk, dev, dt = _append_rows(q_in, k_in, v_in, gamma_q, gamma_k, head_dim, cos_sin, positions, q_out,
+                                               interleaved, stream)
     if hk != heads:
         raise ValueError(f"k_in has {hk} heads, the cache {heads}")
     s = _flat(slots, "slots", T, torch.int64, dev)
-    with _on(dev):
-        st = capi().qknorm_rope_append_kv4(*args, *ptrs, pages, ps, s, eps, _DTYPES[k_in.dtype],
-                                           _stream_handle(stream, dev))
-    _clib.check(st, "qknorm_rope_append_kv4")
+    _call(capi().qknorm_rope_append_kv4, "qknorm_rope_append_kv4", dev, stream, *args, *ptrs, pages, ps, s, eps,
+          _DTYPES[dt])
     return q_out
-
-
-class _Of(NamedTuple):
-    device: torch.device
-    dtype: torch.dtype
 
 
 def qknorm_kv4_read(cache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16, *, k_out=None, v_out=None,
                     stream=None):
     """The cached tokens at ``slots`` as K and V rows ``[n, kv_heads * head_dim]``
     of ``dtype`` (zeros for a slot outside the cache)."""
-    dev = slots.device
+    if not isinstance(slots, _Tensor) or not slots.is_cuda:
+        raise ValueError("slots must be a CUDA tensor (this library has no CPU path)")
+    dev, n = slots.get_device(), slots.numel()
     ptrs, (pages, ps, hk, d) = _kv4_args(cache, dev)
     if dtype not in (torch.float32, torch.bfloat16, torch.float16):
         raise TypeError(f"dtype {dtype} unsupported (float32, bfloat16, float16)")
-    n = slots.numel()
     s = _flat(slots, "slots", n, torch.int64, dev)
     W = hk * d
     made = []
     if k_out is None:
-        made.append(k_out := torch.empty((n, W), dtype=dtype, device=dev))
+        made.append(k_out := slots.new_empty((n, W), dtype=dtype))
         sk = W
     else:
-        sk = _match(k_out, "k_out", _Of(dev, dtype), n, W)
+        sk = _match(k_out, "k_out", dev, dtype, n, W)
     if v_out is None:
-        made.append(v_out := k_out.new_empty((n, W)))
+        made.append(v_out := slots.new_empty((n, W), dtype=dtype))
         sv = W
     else:
-        sv = _match(v_out, "v_out", _Of(dev, dtype), n, W)
+        sv = _match(v_out, "v_out", dev, dtype, n, W)
     _used_on(stream, *made)
-    with _on(dev):
-        st = capi().qknorm_kv4_read(*ptrs, pages, ps, hk, d, s, n, k_out.data_ptr(), sk, v_out.data_ptr(), sv,
-                                    _DTYPES[dtype], _stream_handle(stream, dev))
-    _clib.check(st, "qknorm_kv4_read")
+    _call(capi().qknorm_kv4_read, "qknorm_kv4_read", dev, stream, *ptrs, pages, ps, hk, d, s, n, k_out.data_ptr(), sk,
+          v_out.data_ptr(), sv, _DTYPES[dtype])
     return k_out, v_out
 
 
@@ -363,8 +368,7 @@ def qknorm_kv4_attention(q: torch.Tensor, cache, block_table: torch.Tensor, seq_
     knows (longer sequences are cut there).  ``window`` > 0 limits a row to that
     many last tokens.  Rows of no sequence are left as they were in ``out`` and
     ``lse`` (unspecified where these are made here)."""
-    T, W, sq = _rows(q, "q")
-    dev, dt = q.device, q.dtype
+    T, W, sq, dev, dt = _first(q, "q")
     ptrs, (pages, ps, hk, d) = _kv4_args(cache, dev)
     hq = _heads(W, d, "q")
     if not isinstance(block_table, torch.Tensor) or len(block_table.shape) != 2:
@@ -379,11 +383,11 @@ def qknorm_kv4_attention(q: torch.Tensor, cache, block_table: torch.Tensor, seq_
         made.append(out := q.new_empty((T, W)))
         so = W
     else:
-        so = _match(out, "out", q, T, W)
+        so = _match(out, "out", dev, dt, T, W)
     if lse is not None:
         lp = _flat(lse, "lse", T * hq, torch.float32, dev)
     elif return_lse:
-        made.append(lse := torch.empty((T, hq), dtype=torch.float32, device=dev))
+        made.append(lse := q.new_empty((T, hq), dtype=torch.float32))
         lp = lse.data_ptr()
     else:
         lp = None
@@ -399,9 +403,7 @@ def qknorm_kv4_attention(q: torch.Tensor, cache, block_table: torch.Tensor, seq_
         ws, ws_bytes = _workspace(workspace, dev)
     _used_on(stream, *made)
     scale = 1.0 / math.sqrt(d) if softmax_scale is None else softmax_scale
-    with _on(dev):
-        st = lib.qknorm_kv4_attention(q.data_ptr(), sq, out.data_ptr(), so, lp, hq, *ptrs, pages, ps, hk, d, bt,
-                                      max_pages, sl, qs, T, B, max_q_len, max_seq_len, window, scale, ws, ws_bytes,
-                                      _DTYPES[dt], _stream_handle(stream, dev))
-    _clib.check(st, "qknorm_kv4_attention")
+    _call(lib.qknorm_kv4_attention, "qknorm_kv4_attention", dev, stream, q.data_ptr(), sq, out.data_ptr(), so, lp, hq,
+          *ptrs, pages, ps, hk, d, bt, max_pages, sl, qs, T, B, max_q_len, max_seq_len, window, scale, ws, ws_bytes,
+          _DTYPES[dt])
     return (out, lse) if return_lse else out

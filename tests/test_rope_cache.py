@@ -963,6 +963,15 @@ def test_wrappers_refuse_host_tensors():
     x, one, cs = torch.zeros((2, 128)), torch.ones(64), table(4, 64)
     with pytest.raises(ValueError, match="CUDA"):
         qk.qknorm_headwise_rope(x, x, one, one, 64, cs, torch.zeros(2, dtype=torch.int64))
+    cache = qk.kv4_cache(2, 16, 1, 128, "cpu")
+    with pytest.raises(ValueError, match="CUDA"):
+        qk.qknorm_kv4_read(cache, torch.zeros(2, dtype=torch.int64))
+    with pytest.raises(ValueError, match="CUDA"):
+        qk.qknorm_rope_append_kv4(None, x, x, one, one, cs, torch.zeros(2, dtype=torch.int64), cache,
+                                  torch.zeros(2, dtype=torch.int64))
+    with pytest.raises(ValueError, match="CUDA"):
+        qk.qknorm_kv4_attention(x.bfloat16(), cache, torch.zeros((2, 1), dtype=torch.int32),
+                                torch.zeros(2, dtype=torch.int32), max_seq_len=16)
     with pytest.raises(ValueError):
         qk.kv4_cache(2, 8, 1, 128, "cpu")
     with pytest.raises(ValueError):
