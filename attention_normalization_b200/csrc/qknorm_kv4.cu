@@ -123,6 +123,11 @@ __device__ __forceinline__ float finish_lse(float m, float total) {  // base 2 -
 // The reference exponent moves only when a scaled weight would exceed 2^15, or a
 // weight 2^75 where the values are (nearly) zeros: one vote per step.  The exact
 // maximum is not needed, as l and O share the reference.
+// Instructions bound it: 300 a warp for 16 tokens of 128 dims and 8 rows, 146 of
+// them codes to halves and 16 products (one B200: one token for each of 64
+// sequences of 1024 to 4096 tokens, 32 heads over 8, 60 us, 3.0 TB/s; one of
+// 131072 tokens 45 us, 3.2 TB/s; the loads alone take 47 and 41 us).  4 warps a
+// CTA: with 8 the batch took 72 us.
 constexpr int kAttnWarps = 4;
 constexpr int kLeastShare = 32;  // tiles: 8 for each warp
 // What beginning and ending a unit costs a CTA, in tiles: shares are equal in
@@ -680,7 +685,9 @@ __device__ __forceinline__ Share find_share(const Kv4AttnParams &p, int tile_row
     return found;
 }
 
-// CTAs resident on an SM: what 64 K registers hold.
+// CTAs resident on an SM.  Of 128 dims three: with 8 rows (158 registers) 131072
+// tokens take 46 us where four (128 registers) take 50, with 16 rows chunks take
+// 340 us where two (no spills) take 386.
 template <int D, int NT>
 constexpr int kResident = D == 64 ? (NT == 1 ? 5 : 4) : D == 128 ? 3 : 2;
 
@@ -811,14 +818,24 @@ constexpr int kSms = 148;
 Plan plan(int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t max_q_len, int32_t max_seq_len) {
     Plan pl{};
     const int64_t rows = (int64_t)max_q_len * (q_heads / kv_heads);
-    pl.n_tiles = rows <= 8 || head_dim == 256 ? 1 : 2;  // 16 rows of 256 dims do not fit the registers
+    // 16 rows where there are more than 8 (4 sequences' chunks of 509 rows, 128 dims: 340 us, 470 us with 8 rows;
+    // two tokens of 8 heads each: 37 against 40 us); of 256 dims they do not fit the registers
+    pl.n_tiles = rows <= 8 || head_dim == 256 ? 1 : 2;
     pl.row_tiles = (int32_t)((rows + 8 * pl.n_tiles - 1) / (8 * pl.n_tiles));
     pl.pairs = (int64_t)B * pl.row_tiles;
     const int64_t units = pl.pairs * kv_heads, tiles = ((int64_t)max_seq_len + 15) / 16;
     const int resident = pl.n_tiles == 1 ? (head_dim == 64 ? kResident<64, 1> : head_dim == 128 ? kResident<128, 1> : kResident<256, 1>)
                                          : (head_dim == 64 ? kResident<64, 2> : head_dim == 128 ? kResident<128, 2> : 2);
     const int64_t slots = (int64_t)kSms * resident;
-    if (units >= 4 * slots || tiles <= 2 * kLeastShare || units * (tiles + kUnitCost) >= ((int64_t)1 << 31)) return pl;
+    // One CTA a unit where units are many, or short enough that shares and a join
+    // cost more than their balance gains (whole units against shares, one token a
+    // sequence, 32 heads over 8 of 128: 128 sequences to 4096 tokens 104 against
+    // 107 us, 128 to 2048 60 against 69, 64 to 4096 65 against 60.5, 64 to 2048
+    // 38.5 against 40.9, 64 to 1024 24.7 against 30.5, 16 to 8192 59 against 36,
+    // 4 to 2048 17.7 against 12.4, 4 to 1024 10.5 against 12.5).
+    if (units >= 2 * slots || tiles <= 64 || (units >= slots && tiles <= 128) ||
+        units * (tiles + kUnitCost) >= ((int64_t)1 << 31))
+        return pl;
     const int64_t most = (units * (tiles + kUnitCost) + kLeastShare - 1) / kLeastShare;
     pl.ctas = (int32_t)(most < slots ? most : slots);
     return pl;
