@@ -474,9 +474,10 @@ __device__ __forceinline__ bool turned(const LanePlace<E> &at, int i, int n) {
     return (i < n / 2 ? at.pair_lo : at.pair_hi) >= 0;
 }
 
-// One head: the lane's parted vectors to normed and turned elements.
+// One head: the lane's parted vectors to normed and turned elements.  Returns r
+// (1 without a norm).
 template <typename E, int L>
-__device__ __forceinline__ void lane_forward(const RopeParams &p, const LanePlace<E> &at, bool norm,
+__device__ __forceinline__ float lane_forward(const RopeParams &p, const LanePlace<E> &at, bool norm,
                                              const PairFactors<Elem<E>::kPerVec / 2> &f, const uint4 &va, const uint4 &vb,
                                              F2 (&a)[Elem<E>::kPerVec / 2], F2 (&b)[Elem<E>::kPerVec / 2]) {
     constexpr int N = Elem<E>::kPerVec / 2;
@@ -504,6 +505,7 @@ __device__ __forceinline__ void lane_forward(const RopeParams &p, const LanePlac
         a[i] = mul2(fa, rr);
         b[i] = mul2(fb, rr);
     }
+    return r;
 }
 
 // ----------------------------------------------------------------------------
@@ -558,12 +560,15 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // 32 bits, u = 2^-24: at most 10 u of the element (the squared sum's 11
 // additions halved, 4 for the root's 2 ulp, one for the last product) and 4 u of
 // the head's largest (two roundings of each product times |a cos| + |b sin| <=
-// sqrt(2) that largest, and one of their sum).  Returns the lanes (as a mask) for
-// whose heads a scale or a code lies nearer than that to a border, so that 64
-// bits have to decide, or a scale is outside fp16's normal range; nothing of
-// those heads is stored.
+// sqrt(2) that largest, and one of their sum).  That holds for an r in (0, 2^50):
+// r is 0 where the squared sum has passed fp32's largest number, and from 2^50
+// on squares, or elements before their product with r, may have been subnormals,
+// which have fewer bits.  Returns the lanes (as a mask) for whose heads a scale
+// or a code lies nearer than that to a border, so that 64 bits have to decide, r
+// lies outside, or a scale is outside fp16's normal range; nothing of those heads
+// is stored.
 template <typename E, int L>
-__device__ __forceinline__ uint32_t lane_quantise(const RopeParams &p, bool formed, int u, bool there, const LanePlace<E> &at,
+__device__ __forceinline__ uint32_t lane_quantise(const RopeParams &p, bool formed, float r, int u, bool there, const LanePlace<E> &at,
                                               const F2 (&a)[Elem<E>::kPerVec / 2], const F2 (&b)[Elem<E>::kPerVec / 2],
                                               uint8_t *codes, __half *scales) {
     constexpr int V = Elem<E>::kPerVec, N = V / 2, H = N / 2;
@@ -584,7 +589,7 @@ __device__ __forceinline__ uint32_t lane_quantise(const RopeParams &p, bool form
     const float own = formed ? 10.0f * kU : 0.0f;
     constexpr int groups = L * 2 * V / kKv4Group;  // the lanes hold the head exactly
     const int group_lo = at.lo / kKv4Group, group_hi = at.hi / kKv4Group;
-    bool near = f2_lo(zero) != 0.0f || f2_hi(zero) != 0.0f;
+    bool near = f2_lo(zero) != 0.0f || f2_hi(zero) != 0.0f || !(r > 0.0f && r < 1.125899907e15f);
     float slo = 0.0f, shi = 0.0f;
     __half held = __float2half(0.0f);
 #pragma unroll
@@ -721,14 +726,15 @@ __device__ __forceinline__ void heads_to_kv4(const RopeParams &p, const WarpHead
         if (turn == kTurnRow) {
             if (p.interleaved) part_pairs<E>(va, vb);
             F2 a[V / 2], b[V / 2];
+            float r = 1.0f;
             if (kv == 0) {
-                lane_forward<E, L>(p, at, p.gamma[1] != nullptr, f, va, vb, a, b);
+                r = lane_forward<E, L>(p, at, p.gamma[1] != nullptr, f, va, vb, a, b);
             } else {
                 Elem<E>::widen(va, a);
                 Elem<E>::widen(vb, b);
             }
             const int64_t cell = (page * p.heads[1] + w.h + from) * p.page_size + off;
-            unsure = lane_quantise<E, L>(p, kv == 0, u, there, at, a, b,
+            unsure = lane_quantise<E, L>(p, kv == 0, r, u, there, at, a, b,
                                          reinterpret_cast<uint8_t *>(p.cache[kv]) + cell * (p.head_dim / 2),
                                          p.scales[kv] + cell * (p.head_dim / kKv4Group));
         }
