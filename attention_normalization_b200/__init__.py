@@ -99,6 +99,20 @@ def _stream_handle(stream, device) -> int:
     return int(stream)
 
 
+def _used_on(stream, *tensors):
+    """Tensors allocated here on the current stream but used on `stream` (a
+    torch stream or a raw handle): the allocator must not hand them out again
+    before that stream is done."""
+    if stream is None or not tensors:
+        return
+    if not isinstance(stream, torch.cuda.Stream):
+        handle, index = int(stream), tensors[0].get_device()
+        # 0 is the legacy default stream; ExternalStream would make a stream of its own of it
+        stream = torch.cuda.ExternalStream(handle, index) if handle else torch.cuda.default_stream(index)
+    for t in tensors:
+        t.record_stream(stream)
+
+
 class _NoSwitch:
     def __enter__(self):
         return None

@@ -18,7 +18,7 @@ from typing import NamedTuple
 
 import torch
 
-from . import _DTYPES, _clib, _on, _raw_current_stream, _rows, _stream_handle, capi, gamma_dtype
+from . import _DTYPES, _clib, _on, _raw_current_stream, _rows, _stream_handle, _used_on, capi, gamma_dtype
 
 # These calls are short on the GPU, so what they look at on the host is kept
 # small: each operand once, its device as a number, what is made here not at all.
@@ -91,14 +91,6 @@ def _heads(width, head_dim, name):
     if head_dim < 1 or width % head_dim:
         raise ValueError(f"{name}: the row width must be a whole number of heads of head_dim elements")
     return width // head_dim
-
-
-def _used_on(stream, *tensors):
-    """Tensors allocated here on the current stream but used on `stream`: the
-    allocator must not hand them out again before that stream is done."""
-    if isinstance(stream, torch.cuda.Stream):
-        for t in tensors:
-            t.record_stream(stream)
 
 
 def qknorm_headwise_rope(q_in: torch.Tensor, k_in: torch.Tensor, gamma_q: torch.Tensor, gamma_k: torch.Tensor,

@@ -9,7 +9,8 @@ import torch
 
 import attention_normalization_b200 as qk
 import test_rope_cache as rc
-from test_rope_cache import BF16, DEV, EPS, F16, F32
+from attention_normalization_b200 import rope_cache
+from test_rope_cache import BF16, DEV, EPS, F32
 
 
 # --------------------------------------------------------------------------- 4-bit append
@@ -42,3 +43,71 @@ def test_append_kv4_of_keys_whose_squared_sum_leaves_fp32(eps, sizes, D, rot, in
         c, s = rc.quantise(want.numpy())
         assert torch.equal(scales.cpu()[slots // ps, :, slots % ps], torch.from_numpy(s))
         assert torch.equal(rc.unpack(codes.cpu())[slots // ps, :, slots % ps], torch.from_numpy(c))
+
+
+# --------------------------------------------------------------------------- streams
+
+def test_tensors_made_for_a_raw_stream_handle_are_recorded(monkeypatch):
+    """What a call allocates and drops is kept by the allocator until a stream
+    given as an integer is done with it, as for a torch stream."""
+    made = []
+
+    class External:
+        def __init__(self, handle, device):
+            made.append((handle, device))
+
+    class Held:
+        def __init__(self):
+            self.streams = []
+
+        def get_device(self):
+            return 3
+
+        def record_stream(self, s):
+            self.streams.append(s)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", External)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device: ("default", device))
+    a, b = Held(), Held()
+    rope_cache._used_on(0x7F00, a, b)
+    assert made == [(0x7F00, 3)] and len(a.streams) == len(b.streams) == 1
+    assert isinstance(a.streams[0], External) and a.streams[0] is b.streams[0]
+    rope_cache._used_on(0, a)
+    assert a.streams[1] == ("default", 3)
+    rope_cache._used_on(None, a)
+    rope_cache._used_on(0x7F00)
+    assert len(a.streams) == 2 and len(made) == 1
+
+
+@pytest.mark.gpu
+def test_workspaces_of_calls_on_a_raw_stream_handle():
+    """Attention over a split cache and a gradient on a stream given as an
+    integer that is still busy, while the current stream allocates and fills
+    buffers of the sizes of the workspaces that the calls have dropped."""
+    g = torch.Generator().manual_seed(15)
+    hq, hk, D, ps, L, T = 8, 2, 128, 64, 9000, 700
+    pages = -(-L // ps)
+    bt, lens = torch.arange(pages, dtype=torch.int32, device=DEV).view(1, -1), torch.tensor([L], dtype=torch.int32, device=DEV)
+    cache = rc.random_cache(pages, ps, hk, D, g)
+    q = torch.randn((1, hq * D), generator=g).to(BF16).to(DEV)
+    x, dy = (torch.randn((T, hq * D), generator=g).to(BF16).to(DEV) for _ in range(2))
+    gm, cs, pos = rc.gamma_of(D, BF16, g).to(DEV), rc.table(T, D).to(DEV), torch.arange(T, device=DEV)
+    sizes = [qk.kv4_attention_workspace_bytes(1, 1, hq, hk, D, 1, L), qk.rope_backward_workspace_bytes(T, hq, hq, D)]
+    assert min(sizes) > 0
+    big = torch.empty(1 << 28, dtype=torch.uint8, device=DEV)
+
+    def calls(stream):
+        return [qk.qknorm_kv4_attention(q, cache, bt, lens, max_seq_len=L, stream=stream),
+                *qk.qknorm_headwise_rope_backward(dy, dy, x, x, gm, gm, D, cs, pos, stream=stream)]
+    alone = calls(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        with torch.cuda.stream(side):
+            for _ in range(8):
+                big.zero_()  # keeps the stream busy until the buffers below are filled
+        got = calls(side.cuda_stream)
+        fill = [torch.empty(n, dtype=torch.uint8, device=DEV).fill_(0xFF) for n in sizes for _ in range(3)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, alone):
+            assert torch.equal(a, b)
+        del fill
