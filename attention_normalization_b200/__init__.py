@@ -287,6 +287,7 @@ def qknorm_qkv_projection(x: torch.Tensor, w: torch.Tensor, gamma_q: torch.Tenso
     need = qkv_workspace_bytes(T, Hq, Hk) if Hq % QKV_TILE_N == 0 and Hk % QKV_TILE_N == 0 else 0
     if workspace is None:
         workspace = torch.empty((max(need, 4) // 4,), dtype=torch.float32, device=dev)
+        _used_on(stream, workspace)
     if not (workspace.is_cuda and workspace.device == dev and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor on the device of x")
     gq = _vec(gamma_q, "gamma_q", Hq, torch.bfloat16, dev)

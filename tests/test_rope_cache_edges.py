@@ -111,3 +111,30 @@ def test_workspaces_of_calls_on_a_raw_stream_handle():
         for a, b in zip(got, alone):
             assert torch.equal(a, b)
         del fill
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("raw", [False, True])
+def test_workspace_of_a_projection_on_another_stream(raw):
+    """The partial sums that the projection makes room for and drops, on a busy
+    stream, while the current stream allocates and fills buffers of their size."""
+    g = torch.Generator().manual_seed(16)
+    T, Dm, Hq, Hk = 512, 256, 512, 256
+    x = torch.randn((T, Dm), generator=g).to(BF16).to(DEV)
+    w = (torch.randn((Hq + 2 * Hk, Dm), generator=g) / 16).to(BF16).to(DEV)
+    gq, gk = rc.gamma_of(Hq, BF16, g).to(DEV), rc.gamma_of(Hk, BF16, g).to(DEV)
+    n = qk.qkv_workspace_bytes(T, Hq, Hk)
+    assert n > 0
+    big = torch.empty(1 << 28, dtype=torch.uint8, device=DEV)
+    alone = qk.qknorm_qkv_projection(x, w, gq, gk, Hq, Hk, Hk)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        with torch.cuda.stream(side):
+            for _ in range(8):
+                big.zero_()
+        got = qk.qknorm_qkv_projection(x, w, gq, gk, Hq, Hk, Hk, stream=side.cuda_stream if raw else side)
+        fill = [torch.empty(n, dtype=torch.uint8, device=DEV).fill_(0xFF) for _ in range(3)]
+        torch.cuda.synchronize()
+        assert torch.equal(got, alone)
+        del fill
