@@ -115,14 +115,18 @@ __device__ __forceinline__ float finish_lse(float m, float total) {  // base 2 -
 //
 // Queries are scaled by a power of two per row to fit halves without loss
 // (elements 2^-24 below the row's largest lose bits that fp32 sums of the row
-// would not see either).  Weights are rounded to halves, 2^-11 relative; they
-// are kept between 2^-31 and 2^8 of the reference by normalising
-// p * (value scale), not p alone, and by an offset of 2^7.  The row sum l takes
-// the unrounded weights.
+// would not see either).  Weights are rounded to halves, 2^-11 relative, for
+// what the tensor cores multiply.  What is rounded is p * (value scale), each
+// group of dims against a reference of its own, the largest such product of the
+// row so far, kept at 2^7 or more: a product loses bits below 2^-21 of it and
+// goes to zero below 2^-32, whatever the other groups' scales are.  (One
+// reference for all groups loses the tail of a group whose scales lie far below
+// another's.)  The row sum l takes the unrounded weights.
 //
-// The reference exponent moves only when a scaled weight would exceed 2^15, or a
-// weight 2^75 where the values are (nearly) zeros: one vote per step.  The exact
-// maximum is not needed, as l and O share the reference.
+// References are whole powers of two, so moving one rounds nothing.  They move
+// only when a scaled weight would exceed 2^15, or a weight 2^75 where the values
+// are (nearly) zeros: one vote per step.  The exact maximum is not needed, as O
+// has its group's reference until the end and l the first group's.
 // Instructions bound it: 300 a warp for 16 tokens of 128 dims and 8 rows, 146 of
 // them codes to halves and 16 products (one B200: one token for each of 64
 // sequences of 1024 to 4096 tokens, 32 heads over 8, 60 us, 3.0 TB/s; one of
@@ -134,7 +138,7 @@ constexpr int kLeastShare = 32;  // tiles: 8 for each warp
 // tiles and units alike (64 sequences of 1024 to 4096 tokens, 8 KV heads: 63.4 us
 // without this, 60.3 us with it).
 constexpr int kUnitCost = 16;
-constexpr float kOffset = 7.0f, kLargest = 32768.0f;
+constexpr float kOffset = 8.0f, kLargest = 32768.0f, kMostWeight = 3.7778931862957162e22f;  // 2^75
 
 template <int D>
 struct Kv4Tile {  // bytes of one 16-token tile of one KV head
@@ -373,9 +377,11 @@ __device__ __forceinline__ void attend_unit(const Kv4AttnParams &p, const Seq &s
     const int lowest = base_pos + small_div(r0, p.group);                                    // the tile's first row
     const int highest = base_pos + small_div(min(r0 + R, rows) - 1, p.group);
 
-    // ref: kOffset - the rows' reference exponents (infinity: none yet; rows that see nothing need none)
+    // ref: kOffset - the rows' reference exponents for l and the first group (infinity: none yet; rows that see
+    // nothing need none); apart: the other groups' references over it, as powers of two (2^-41 to 2^41)
     float o[NT][D / 16][4] = {};
     float ref[NT][2], l[NT][2];
+    F2 apart[NT][G];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -383,6 +389,10 @@ __device__ __forceinline__ void attend_unit(const Kv4AttnParams &p, const Seq &s
             ref[j][e] = r0 + 8 * j + 2 * c + e < rows && top[j][e] >= 0 ? INFINITY : kOffset;
             l[j][e] = 0.0f;
         }
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) apart[j][gr] = f2(1.0f, 1.0f);
     bool unset = true;  // some row has no reference yet
     int stage = 0;
 #pragma unroll 1
@@ -443,7 +453,7 @@ __device__ __forceinline__ void attend_unit(const Kv4AttnParams &p, const Seq &s
             // weights: packed products with the value scales, and what l grows by
             uint32_t pk[H][NT][G][2];
             float grown[H][NT][2];
-            float big = 0.0f;
+            float big = 0.0f, most = 0.0f;
             auto weigh = [&](int h, int j, uint32_t hide) {
                 float w[4];
 #pragma unroll
@@ -451,13 +461,16 @@ __device__ __forceinline__ void attend_unit(const Kv4AttnParams &p, const Seq &s
                     w[e] = hide >> e & 1u ? 0.0f : ex2(fmaf(s[h][j][e], qmul[j][e & 1], ref[j][e & 1]));
                 grown[h][j][0] = w[0] + w[2];
                 grown[h][j][1] = w[1] + w[3];
-                big = fmaxf(big, fmaxf(grown[h][j][0], grown[h][j][1]) * 8.6736174e-19f);  // 2^-60: where the values are zeros
+                most = fmaxf(most, fmaxf(grown[h][j][0], grown[h][j][1]));
 #pragma unroll
                 for (int gr = 0; gr < G; ++gr) {
                     float x[4];
+                    const F2 lo = gr == 0 ? f2(w[0], w[1]) : mul2(f2(w[0], w[1]), apart[j][gr]);
+                    const F2 hi = gr == 0 ? f2(w[2], w[3]) : mul2(f2(w[2], w[3]), apart[j][gr]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {  // a hidden token's scale may be anything
-                        x[e] = hide >> e & 1u ? 0.0f : w[e] * vscale[h][gr][e >> 1];
+                        const F2 of = e < 2 ? lo : hi;
+                        x[e] = hide >> e & 1u ? 0.0f : (e & 1 ? f2_hi(of) : f2_lo(of)) * vscale[h][gr][e >> 1];
                         big = fmaxf(big, x[e]);
                     }
                     pk[h][j][gr][0] = pack_half2(x[0], x[1]);
@@ -487,41 +500,49 @@ __device__ __forceinline__ void attend_unit(const Kv4AttnParams &p, const Seq &s
 #pragma unroll
                     for (int j = 0; j < NT; ++j) weigh(h, j, 0u);
             }
-            if (unset || __any_sync(0xFFFFFFFFu, big > kLargest)) {
-                float lv[H][2];  // log2 of each token's largest value scale, kept to what halves can hold
+            if (unset || __any_sync(0xFFFFFFFFu, big > kLargest || most > kMostWeight)) {
+                float lv[H][G][2];  // log2 of the value scales, kept to what halves can hold
 #pragma unroll
                 for (int h = 0; h < H; ++h)
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        float v = vscale[h][0][t];
+                    for (int gr = 0; gr < G; ++gr)
 #pragma unroll
-                        for (int gr = 1; gr < G; ++gr) v = fmaxf(v, vscale[h][gr][t]);
-                        lv[h][t] = fminf(fmaxf(lg2(v), -24.0f), 16.0f);
-                    }
+                        for (int t = 0; t < 2; ++t) lv[h][gr][t] = fminf(fmaxf(lg2(vscale[h][gr][t]), -24.0f), 16.0f);
                 bool none = false;
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float y = -INFINITY;
+                        const float before = ref[j][e];
 #pragma unroll
-                        for (int h = 0; h < H; ++h)
+                        for (int gr = 0; gr < G; ++gr) {
+                            float y = -INFINITY;
 #pragma unroll
-                            for (int t = 0; t < 2; ++t)
-                                if (!(hidden >> (4 * (NT * h + j) + 2 * t + e) & 1u))
-                                    y = fmaxf(y, fmaf(s[h][j][2 * t + e], qmul[j][e], lv[h][t]));
-                        y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 4));
-                        y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 8));
-                        y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 16));
-                        const float r = fminf(ref[j][e], kOffset - y);
-                        const float f = r == ref[j][e] ? 1.0f : ex2(r - ref[j][e]);
-                        ref[j][e] = r;
-                        none |= r == INFINITY;
-                        l[j][e] *= f;
+                            for (int h = 0; h < H; ++h)
 #pragma unroll
-                        for (int i = 0; i < D / 16; ++i) {
-                            o[j][i][e] *= f;
-                            o[j][i][e + 2] *= f;
+                                for (int t = 0; t < 2; ++t)
+                                    if (!(hidden >> (4 * (NT * h + j) + 2 * t + e) & 1u))
+                                        y = fmaxf(y, fmaf(s[h][j][2 * t + e], qmul[j][e], lv[h][gr][t]));
+                            y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 4));
+                            y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 8));
+                            y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, 16));
+                            const float wide = e ? f2_hi(apart[j][gr]) : f2_lo(apart[j][gr]);
+                            const int over = (__float_as_int(wide) >> 23) - 127;
+                            const float was = before + static_cast<float>(over), r = fminf(was, floorf(kOffset - y));
+                            const float f = r == was ? 1.0f : ex2(r - was);
+                            if (gr == 0) {
+                                ref[j][e] = r;
+                                none |= r == INFINITY;
+                                l[j][e] *= f;
+                            } else {  // 2^0 while there is no reference (a NaN becomes the integer 0)
+                                const float now = __int_as_float((static_cast<int>(r - ref[j][e]) + 127) << 23);
+                                apart[j][gr] = e ? f2(f2_lo(apart[j][gr]), now) : f2(now, f2_hi(apart[j][gr]));
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                o[j][4 * gr + i][e] *= f;
+                                o[j][4 * gr + i][e + 2] *= f;
+                            }
                         }
                     }
                 unset = __any_sync(0xFFFFFFFFu, none);
@@ -583,9 +604,12 @@ __device__ __forceinline__ void attend_unit(const Kv4AttnParams &p, const Seq &s
             l[j][e] += __shfl_xor_sync(0xFFFFFFFFu, l[j][e], 16);
             const int r = 8 * j + 2 * c + e;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i)  // dims 64 gr + 8 g + 2 (i % 4), + 1
+            for (int i = 0; i < D / 16; ++i) {  // dims 64 gr + 8 g + 2 (i % 4), + 1, back to the first group's reference
+                const float wide = e ? f2_hi(apart[j][i / 4]) : f2_lo(apart[j][i / 4]);
+                const float f = i < 4 ? 1.0f : __int_as_float((254 << 23) - __float_as_int(wide));
                 *reinterpret_cast<float2 *>(joined + r * D + (i / 4) * 64 + g * 8 + (i % 4) * 2) =
-                    make_float2(o[j][i][e], o[j][i][e + 2]);
+                    make_float2(o[j][i][e] * f, o[j][i][e + 2] * f);
+            }
             if (g == 0) {  // a row whose scores are all NaN has no reference: its sum carries the NaN
                 stat[r] = l[j][e] == 0.0f ? -INFINITY : (ref[j][e] == INFINITY ? 0.0f : -ref[j][e]);
                 stat[R + r] = l[j][e];

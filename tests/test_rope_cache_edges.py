@@ -4,6 +4,8 @@ once, bounds at the ends of their types, streams given as handles.  The formulas
 in 64 bits and their tolerances are test_rope_cache.py's."""
 from __future__ import annotations
 
+import math
+
 import pytest
 import torch
 
@@ -138,3 +140,37 @@ def test_workspace_of_a_projection_on_another_stream(raw):
         torch.cuda.synchronize()
         assert torch.equal(got, alone)
         del fill
+
+
+# --------------------------------------------------------------------------- attention
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,D,scales,n,octaves,strong", [
+    (1, 128, (64.0, 2.0 ** -14), 1020, 8.3, (0, 32, 64, 96)),     # one CTA, a strong token for each of its warps
+    (1, 128, (2.0 ** -14, 64.0), 1020, 8.3, (0, 32, 64, 96)),
+    (4, 128, (2.0 ** -14, 64.0), 1016, 8.3, (0, 32, 64, 96)),     # 16 query rows
+    (1, 256, (2.0 ** -4, 2.0 ** -14, 16.0, 2.0 ** -9), 1020, 8.3, (0, 32, 64, 96)),
+    (1, 128, (1.0, 2.0 ** -13), 131072, 18.2, (0,)),              # cut into shares; the tail is 30% of the weight
+    (4, 128, (2.0 ** -10, 8.0), 30000, 13.62, (20000,)),
+    (1, 256, (2.0 ** -4, 2.0 ** -13, 16.0, 2.0 ** -9), 30000, 13.62, (29999,)),
+    (1, 64, (0.5,), 30000, 13.62, (0,))])
+def test_attention_of_groups_whose_value_scales_are_far_apart(rows, D, scales, n, octaves, strong):
+    """A few strong tokens and a long tail, `octaves` powers of two below them, of
+    equal weights and positive values, so that rounding errors of the weights do
+    not cancel: every group of dims keeps its tail, whatever the other groups'
+    scales are.  Heads at other multiples of the scores come along.  The
+    tolerance counts 2^-11 of each product and 2^-28 of the row's largest for what
+    lies further below."""
+    g = torch.Generator().manual_seed(n + D)
+    ps, hq = 64, 4
+    L = n + rows
+    pages = -(-L // ps)
+    cache = qk.kv4_cache(pages, ps, 1, D, DEV)
+    for t in strong:                                 # codes of 7; the other keys are zeros
+        cache[0][t // ps, 0, t % ps] = 0xFF
+        cache[1][t // ps, 0, t % ps] = octaves * math.log(2.0) / (7 * math.sqrt(D))
+    cache[2].copy_(torch.randint(9, 16, cache[2].shape, generator=g) | torch.randint(9, 16, cache[2].shape, generator=g) << 4)
+    cache[3].copy_(torch.tensor(scales))
+    q = torch.tensor([1.0, 0.5, -1.0, 0.9375]).repeat_interleave(D).repeat(rows, 1).to(BF16).to(DEV)
+    rc.check_attention(q, cache, torch.arange(pages, dtype=torch.int32).view(1, -1), torch.tensor([L], dtype=torch.int32),
+                       torch.tensor([0, rows], dtype=torch.int32), rows, L)
