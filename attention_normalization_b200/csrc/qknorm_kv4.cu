@@ -839,7 +839,8 @@ struct Plan {
 };
 constexpr int kSms = 148;
 
-Plan plan(int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t max_q_len, int32_t max_seq_len) {
+// Query tiles of a call and the CTAs that fit the SMs at once.
+Plan tiled(int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t max_q_len, int64_t *slots) {
     Plan pl{};
     const int64_t rows = (int64_t)max_q_len * (q_heads / kv_heads);
     // 16 rows where there are more than 8 (4 sequences' chunks of 509 rows, 128 dims: 340 us, 470 us with 8 rows;
@@ -847,22 +848,40 @@ Plan plan(int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_
     pl.n_tiles = rows <= 8 || head_dim == 256 ? 1 : 2;
     pl.row_tiles = (int32_t)((rows + 8 * pl.n_tiles - 1) / (8 * pl.n_tiles));
     pl.pairs = (int64_t)B * pl.row_tiles;
+    const int64_t resident = pl.n_tiles == 1 ? (head_dim == 64 ? kResident<64, 1> : head_dim == 128 ? kResident<128, 1> : kResident<256, 1>)
+                                             : (head_dim == 64 ? kResident<64, 2> : head_dim == 128 ? kResident<128, 2> : 2);
+    *slots = kSms * resident;
+    return pl;
+}
+
+int64_t share_ctas(int64_t units, int64_t tiles, int64_t slots) {
+    const int64_t most = (units * (tiles + kUnitCost) + kLeastShare - 1) / kLeastShare;
+    return most < slots ? most : slots;
+}
+
+// Shorter sequences are never cut into shares.
+constexpr int64_t kWholeTiles = 64;
+
+Plan plan(int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t max_q_len, int32_t max_seq_len) {
+    int64_t slots = 0;
+    Plan pl = tiled(B, q_heads, kv_heads, head_dim, max_q_len, &slots);
     const int64_t units = pl.pairs * kv_heads, tiles = ((int64_t)max_seq_len + 15) / 16;
-    const int resident = pl.n_tiles == 1 ? (head_dim == 64 ? kResident<64, 1> : head_dim == 128 ? kResident<128, 1> : kResident<256, 1>)
-                                         : (head_dim == 64 ? kResident<64, 2> : head_dim == 128 ? kResident<128, 2> : 2);
-    const int64_t slots = (int64_t)kSms * resident;
     // One CTA a unit where units are many, or short enough that shares and a join
     // cost more than their balance gains (whole units against shares, one token a
     // sequence, 32 heads over 8 of 128: 128 sequences to 4096 tokens 104 against
     // 107 us, 128 to 2048 60 against 69, 64 to 4096 65 against 60.5, 64 to 2048
     // 38.5 against 40.9, 64 to 1024 24.7 against 30.5, 16 to 8192 59 against 36,
     // 4 to 2048 17.7 against 12.4, 4 to 1024 10.5 against 12.5).
-    if (units >= 2 * slots || tiles <= 64 || (units >= slots && tiles <= 128) ||
+    if (units >= 2 * slots || tiles <= kWholeTiles || (units >= slots && tiles <= 128) ||
         units * (tiles + kUnitCost) >= ((int64_t)1 << 31))
         return pl;
-    const int64_t most = (units * (tiles + kUnitCost) + kLeastShare - 1) / kLeastShare;
-    pl.ctas = (int32_t)(most < slots ? most : slots);
+    pl.ctas = (int32_t)share_ctas(units, tiles, slots);
     return pl;
+}
+
+// Partial outputs and sums of every share's two ends, the pairs' first tiles.
+int64_t share_bytes(int64_t ctas, int64_t pairs, int32_t n_tiles, int32_t head_dim) {
+    return ctas == 0 ? 0 : ctas * 2 * 8 * n_tiles * (head_dim + 2) * 4 + (pairs + 1) * 4;
 }
 
 template <typename E, int D, int NT>
@@ -909,9 +928,14 @@ int64_t qknorm_kv4_attention_workspace_bytes(int64_t T, int32_t B, int32_t q_hea
         q_heads % kv_heads != 0 || head_dim > kRopeMaxHeadDim || T >= ((int64_t)1 << 31) / q_heads)
         return -1;
     if ((int64_t)max_q_len * q_heads > kMaxRows) return -1;
-    const Plan pl = plan(B, q_heads, kv_heads, head_dim, max_q_len, max_seq_len);
-    // partial outputs and sums of every share's two ends, the pairs' first tiles
-    return pl.ctas == 0 ? 0 : (int64_t)pl.ctas * 2 * 8 * pl.n_tiles * (head_dim + 2) * 4 + (pl.pairs + 1) * 4;
+    // enough for every call of at most these sizes: calls that are cut into shares have fewer than 2 * slots units,
+    // of 8 rows more CTAs fit than of 16 but their tiles hold half as many
+    int64_t slots = 0;
+    const Plan pl = tiled(B, q_heads, kv_heads, head_dim, max_q_len, &slots);
+    const int64_t tiles = ((int64_t)max_seq_len + 15) / 16;
+    if (tiles <= kWholeTiles) return 0;
+    const int64_t units = pl.pairs * kv_heads < 2 * slots ? pl.pairs * kv_heads : 2 * slots - 1;
+    return share_bytes(share_ctas(units, tiles, slots), units / kv_heads, pl.n_tiles, head_dim);
 }
 
 qkn_status qknorm_kv4_attention(const void *q, int64_t q_stride, void *out, int64_t out_stride, float *lse,
@@ -948,13 +972,12 @@ qkn_status qknorm_kv4_attention(const void *q, int64_t q_stride, void *out, int6
         return fail(QKN_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
     if ((int64_t)max_q_len * q_heads > kMaxRows)
         return fail(QKN_ERR_UNSUPPORTED, "max_q_len = %d too long: call in chunks of rows", max_q_len);
-    const int64_t need = qknorm_kv4_attention_workspace_bytes(T, B, q_heads, kv_heads, head_dim, max_q_len, max_seq_len);
-    if (need < 0) return fail(QKN_ERR_INVALID_ARG, "sizes out of range");
+    const Plan pl = plan(B, q_heads, kv_heads, head_dim, max_q_len, max_seq_len);
+    const int64_t need = share_bytes(pl.ctas, pl.pairs, pl.n_tiles, head_dim);
     if (workspace_bytes < need || (need > 0 && !workspace))
         return fail(QKN_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)need);
     if (need > 0 && !aligned16(workspace)) return fail(QKN_ERR_INVALID_ARG, "the workspace must be 16-byte aligned");
     if (T == 0 || B == 0) return ok();
-    const Plan pl = plan(B, q_heads, kv_heads, head_dim, max_q_len, max_seq_len);
     Span w[3], r[8];
     int nw = 0, nr = 0;
     w[nw++] = Span{out, width * 2, out_stride * 2, T, "out"};

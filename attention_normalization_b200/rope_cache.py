@@ -341,7 +341,8 @@ def qknorm_kv4_read(cache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloa
 
 def kv4_attention_workspace_bytes(T: int, batch: int, q_heads: int, kv_heads: int, head_dim: int, max_q_len: int,
                                   max_seq_len: int) -> int:
-    """Workspace ``qknorm_kv4_attention`` needs for these bounds."""
+    """Workspace that serves every ``qknorm_kv4_attention`` with these heads and
+    at most this batch, ``max_q_len`` and ``max_seq_len``."""
     n = capi().qknorm_kv4_attention_workspace_bytes(T, batch, q_heads, kv_heads, head_dim, max_q_len, max_seq_len)
     if n < 0:
         raise ValueError("invalid sizes for the attention's workspace")

@@ -398,7 +398,11 @@ qkn_status qknorm_kv4_attention(const void *q, int64_t q_stride, void *out, int6
                                 const int32_t *seq_lens, const int32_t *q_start, int64_t T, int32_t B,
                                 int32_t max_q_len, int32_t max_seq_len, int32_t window, float scale, void *workspace,
                                 int64_t workspace_bytes, qkn_dtype dtype, void *stream);
-/* Bytes of its workspace (0 when the cache is not split); -1 for bad sizes. */
+/*
+ * Bytes of workspace that serve every call with these heads and at most this B,
+ * max_q_len and max_seq_len, whatever shape it has (0: none of them needs any);
+ * -1 for bad sizes.
+ */
 int64_t qknorm_kv4_attention_workspace_bytes(int64_t T, int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                              int32_t max_q_len, int32_t max_seq_len);
 

@@ -11,7 +11,8 @@ import torch
 
 import attention_normalization_b200 as qk
 import test_rope_cache as rc
-from attention_normalization_b200 import rope_cache
+from attention_normalization_b200 import _clib, rope_cache
+from attention_normalization_b200 import build as qbuild
 from test_rope_cache import BF16, DEV, EPS, F32
 
 
@@ -174,3 +175,59 @@ def test_attention_of_groups_whose_value_scales_are_far_apart(rows, D, scales, n
     q = torch.tensor([1.0, 0.5, -1.0, 0.9375]).repeat_interleave(D).repeat(rows, 1).to(BF16).to(DEV)
     rc.check_attention(q, cache, torch.arange(pages, dtype=torch.int32).view(1, -1), torch.tensor([L], dtype=torch.int32),
                        torch.tensor([0, rows], dtype=torch.int32), rows, L)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    qbuild.build(quiet=True)
+    return _clib.load()
+
+
+HEADS = [(32, 8, 128), (8, 8, 64), (32, 8, 64), (6, 2, 256), (20, 1, 128)]
+
+
+@pytest.mark.parametrize("hq,hk,D", HEADS)
+def test_attention_workspace_grows_with_every_bound(lib, hq, hk, D):
+    f = lib.qknorm_kv4_attention_workspace_bytes
+    batches, q_lens, lens = (0, 1, 2, 7, 37, 64, 110, 111, 400, 5000), (1, 2, 3, 8, 9, 50, 400), (0, 1024, 1025, 2048, 2049, 4096, 100000, 1 << 30)
+    size = {(b, n, s): f(1, b, hq, hk, D, n, s) for b in batches for n in q_lens for s in lens}
+    assert min(size.values()) == 0 and 0 < max(size.values()) < 32 << 20
+    for i, b in enumerate(batches):
+        for j, n in enumerate(q_lens):
+            for k, s in enumerate(lens):
+                for key in ((batches[max(i - 1, 0)], n, s), (b, q_lens[max(j - 1, 0)], s), (b, n, lens[max(k - 1, 0)])):
+                    assert size[key] <= size[b, n, s], (key, (b, n, s))
+
+
+@pytest.mark.parametrize("hq,hk,D", HEADS)
+@pytest.mark.parametrize("most", [(120, 1), (120, 5), (5000, 2)])
+def test_attention_workspace_of_the_largest_call_serves_smaller_ones(lib, most, hq, hk, D):
+    """The call's own check, on addresses that nothing reads: it goes on to the
+    launch, which fails for want of a device."""
+    if torch.cuda.is_available():
+        pytest.skip("an accepted call with made-up addresses is not launched")
+    B, n, s = *most, 4096
+    bytes_ = lib.qknorm_kv4_attention_workspace_bytes(B * n, B, hq, hk, D, n, s)
+    for b in (1, 2, 3, 11, 56, 64, 110, 111, B):
+        for m in range(1, n + 1):
+            for t in (s, 2048, 1500, 16):
+                st = lib.qknorm_kv4_attention(*rc.attn_args(
+                    q=rc.at(0), qs=hq * D, out=rc.at(1), os=hq * D, lse=0, hq=hq, hk=hk, D=D, qst=rc.at(10), T=b * m, B=b, mq=m,
+                    ml=t, wb=bytes_))
+                assert st == rc.CUDA, (b, m, t, lib.qknorm_last_error())
+
+
+@pytest.mark.gpu
+def test_one_workspace_for_every_batch():
+    g = torch.Generator().manual_seed(17)
+    hq, hk, D, ps, L, most = 16, 8, 128, 64, 1500, 120
+    pages = -(-L // ps)
+    cache = rc.random_cache(pages, ps, hk, D, g)
+    bt = torch.randint(0, pages, (most, pages), generator=g).int().to(DEV)
+    lens = torch.randint(1, L + 1, (most,), generator=g).int().to(DEV)
+    q = torch.randn((most, hq * D), generator=g).to(BF16).to(DEV)
+    held = torch.empty(qk.kv4_attention_workspace_bytes(most, most, hq, hk, D, 1, L), dtype=torch.uint8, device=DEV)
+    for B in (1, 5, 40, 56, most):
+        args = (q[:B], cache, bt[:B], lens[:B])
+        assert torch.equal(qk.qknorm_kv4_attention(*args, max_seq_len=L, workspace=held),
+                           qk.qknorm_kv4_attention(*args, max_seq_len=L))
