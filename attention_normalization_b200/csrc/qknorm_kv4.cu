@@ -831,6 +831,9 @@ using namespace checks;
 
 // How a call is cut up, from sizes the host knows.
 constexpr int64_t kMaxRows = 1 << 20;  // max_q_len * q_heads
+// Positions lie between -kMaxRows and this; a tile past one and the difference
+// of a position and a window still fit 32 bits.
+constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - ((int64_t)1 << 21);
 
 struct Plan {
     int32_t n_tiles, row_tiles;
@@ -972,6 +975,9 @@ qkn_status qknorm_kv4_attention(const void *q, int64_t q_stride, void *out, int6
         return fail(QKN_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
     if ((int64_t)max_q_len * q_heads > kMaxRows)
         return fail(QKN_ERR_UNSUPPORTED, "max_q_len = %d too long: call in chunks of rows", max_q_len);
+    const int64_t held = (int64_t)max_pages * page_size, longest = held < max_seq_len ? held : max_seq_len;
+    if (longest > kMaxTokens)
+        return fail(QKN_ERR_UNSUPPORTED, "sequences of up to %lld tokens, at most %lld", (long long)longest, (long long)kMaxTokens);
     const Plan pl = plan(B, q_heads, kv_heads, head_dim, max_q_len, max_seq_len);
     const int64_t need = share_bytes(pl.ctas, pl.pairs, pl.n_tiles, head_dim);
     if (workspace_bytes < need || (need > 0 && !workspace))
@@ -1018,7 +1024,7 @@ qkn_status qknorm_kv4_attention(const void *q, int64_t q_stride, void *out, int6
     p.group = q_heads / kv_heads;
     p.max_q_len = max_q_len;
     p.max_seq_len = max_seq_len;
-    p.window = window;
+    p.window = window < longest ? window : 0;  // no token is further back
     p.scale = scale;
     p.q_vector = aligned16(q) && p.q_stride % 16 == 0;
     p.out_vector = ((uintptr_t)out & 7u) == 0 && p.out_stride % 8 == 0;

@@ -388,8 +388,9 @@ qkn_status qknorm_kv4_read(const void *k_codes, const void *k_scales, const void
  * Errors: QKN_ERR_INVALID_ARG for bad sizes, strides, null or unaligned
  * pointers, q_heads not a multiple of kv_heads, an output overlapping another
  * operand, T * q_heads >= 2^31 or a small workspace; QKN_ERR_UNSUPPORTED as
- * above, for more than 65535 sequences, and for max_q_len * q_heads above 2^20
- * (call in chunks of rows).
+ * above, for more than 65535 sequences, for max_q_len * q_heads above 2^20
+ * (call in chunks of rows), and where max_seq_len and max_pages * page_size are
+ * both above 2^31 - 2^21 tokens.
  */
 qkn_status qknorm_kv4_attention(const void *q, int64_t q_stride, void *out, int64_t out_stride, float *lse,
                                 int32_t q_heads, const void *k_codes, const void *k_scales, const void *v_codes,

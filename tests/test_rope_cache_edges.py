@@ -231,3 +231,26 @@ def test_one_workspace_for_every_batch():
         args = (q[:B], cache, bt[:B], lens[:B])
         assert torch.equal(qk.qknorm_kv4_attention(*args, max_seq_len=L, workspace=held),
                            qk.qknorm_kv4_attention(*args, max_seq_len=L))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 5, 21, 20, 19, 1])
+@pytest.mark.parametrize("hq,hk,rows,L", [(4, 2, 30, 20), (16, 1, 30, 20), (2, 2, 1, 20), (8, 1, 3, 1)])
+def test_attention_windows_as_long_as_the_sequence_and_longer(hq, hk, rows, L, window):
+    """With more rows than cached tokens too, whose first rows lie before the sequence."""
+    g = torch.Generator().manual_seed(rows + hq)
+    cache = rc.random_cache(3, 16, hk, 128, g)
+    q = torch.randn((rows, hq * 128), generator=g).to(BF16).to(DEV)
+    rc.check_attention(q, cache, torch.tensor([[2, 0]], dtype=torch.int32), torch.tensor([L], dtype=torch.int32),
+                       torch.tensor([0, rows], dtype=torch.int32), rows, 32, window)
+
+
+@pytest.mark.parametrize("kw,status", [
+    ({"ml": 2 ** 31 - 1}, rc.CUDA), ({"mp": 2 ** 31 - 1}, rc.CUDA), ({"ml": 2 ** 31 - 2 ** 21, "mp": 2 ** 27}, rc.CUDA),
+    ({"ml": 2 ** 31 - 2 ** 21 + 1, "mp": 2 ** 27}, rc.UNSUPPORTED), ({"win": 2 ** 31 - 1}, rc.CUDA)])
+def test_attention_bounds_at_the_ends_of_their_type(lib, kw, status):
+    if torch.cuda.is_available() and status == rc.CUDA:
+        pytest.skip("an accepted call with made-up addresses is not launched")
+    # one sequence: its page table of 2^31 entries stays below the next address
+    st = lib.qknorm_kv4_attention(*rc.attn_args(**{"T": 1, "B": 1, "bt": 1 << 44, **kw}))
+    assert st == status, lib.qknorm_last_error()
