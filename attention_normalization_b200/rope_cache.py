@@ -5,7 +5,11 @@ and errors are stated.
 
 Rows are 2-D views as everywhere in this package.  ``cos_sin`` is the fp32
 table ``[table_rows, rotary_dim]`` (cosines, then sines, of each position),
-``positions`` and ``slots`` are int64 ``[T]``.  A step of serving:
+``positions`` and ``slots`` are int64 ``[T]``.  The calls record nothing for
+autograd and refuse operands that it would have to follow: a training step calls
+them in the ``forward`` of a ``torch.autograd.Function`` (or under
+``torch.no_grad()``) and ``qknorm_headwise_rope_backward`` in its ``backward``.  A
+step of serving:
 
     q = qknorm_rope_append_kv4(q, k, v, gamma_q, gamma_k, cos_sin, positions, cache, slots)
     o = qknorm_kv4_attention(q, cache, block_table, seq_lens, max_seq_len=longest)
@@ -93,12 +97,25 @@ def _heads(width, head_dim, name):
     return width // head_dim
 
 
+_grad_enabled = torch.is_grad_enabled
+
+
+def _untracked(where, *tensors):
+    """Refuses tensors whose gradient autograd follows: outputs would lose it silently."""
+    for t in tensors:
+        if isinstance(t, _Tensor) and t.requires_grad:
+            raise ValueError(f"{where} records nothing for autograd and an operand requires a gradient: call it under "
+                             "torch.no_grad() or in the forward of a torch.autograd.Function")
+
+
 def qknorm_headwise_rope(q_in: torch.Tensor, k_in: torch.Tensor, gamma_q: torch.Tensor, gamma_k: torch.Tensor,
                          head_dim: int, cos_sin: torch.Tensor, positions: torch.Tensor, eps: float = 1e-6, *,
                          interleaved: bool = False, q_out=None, k_out=None, stream=None):
     """Headwise QK-Norm and position rotation of every Q and K head in one
     launch; returns ``(q_out, k_out)``.  ``interleaved`` rotates the pairs
     ``(2i, 2i + 1)`` instead of ``(i, i + rotary_dim / 2)``."""
+    if _grad_enabled():
+        _untracked("qknorm_headwise_rope", q_in, k_in, gamma_q, gamma_k, cos_sin)
     T, Wq, sq, dev, dt = _first(q_in, "q_in")
     Tk, Wk, sk = _like(k_in, "k_in", dev, dt)
     if T != Tk:
@@ -147,6 +164,8 @@ def qknorm_headwise_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q_
     gradients of its outputs, ``q_in`` and ``k_in`` the rows it read.  Returns
     ``(dq_in, dk_in, dgamma_q, dgamma_k)``, the last two fp32 ``[head_dim]``
     summed over tokens and heads (overwritten, not accumulated)."""
+    if _grad_enabled():  # a gradient of this gradient
+        _untracked("qknorm_headwise_rope_backward", dq_out, dk_out)
     T, Wq, sq, dev, dt = _first(q_in, "q_in")
     Tk, Wk, sk = _like(k_in, "k_in", dev, dt)
     if T != Tk:
@@ -238,6 +257,8 @@ def qknorm_rope_append(q_in, k_in: torch.Tensor, v_in: torch.Tensor, gamma_q, ga
     place ``slots[t] % page_size``, and nowhere where that lies outside the
     cache.  ``gamma_q`` and ``gamma_k`` of ``None`` leave the norm out, ``q_in``
     of ``None`` the Q rows."""
+    if _grad_enabled():
+        _untracked("qknorm_rope_append", q_in, k_in, v_in, gamma_q, gamma_k, cos_sin)
     args, q_out, T, hk, dev, dt = _append_rows(q_in, k_in, v_in, gamma_q, gamma_k, head_dim, cos_sin, positions, q_out,
                                                interleaved, stream)
     pages = k_cache.shape[:2]
@@ -297,6 +318,8 @@ def qknorm_rope_append_kv4(q_in, k_in: torch.Tensor, v_in: torch.Tensor, gamma_q
                            positions: torch.Tensor, cache, slots: torch.Tensor, eps: float = 1e-6, *,
                            interleaved: bool = False, q_out=None, stream=None):
     """``qknorm_rope_append`` into a 4-bit cache (``kv4_cache``); returns ``q_out``."""
+    if _grad_enabled():
+        _untracked("qknorm_rope_append_kv4", q_in, k_in, v_in, gamma_q, gamma_k, cos_sin)
     if not isinstance(k_in, _Tensor) or not k_in.is_cuda:
         raise ValueError("k_in must be a CUDA tensor (this library has no CPU path)")
     ptrs, (pages, ps, heads, head_dim) = _kv4_args(cache, k_in.get_device())
@@ -361,6 +384,8 @@ def qknorm_kv4_attention(q: torch.Tensor, cache, block_table: torch.Tensor, seq_
     knows (longer sequences are cut there).  ``window`` > 0 limits a row to that
     many last tokens.  Rows of no sequence are left as they were in ``out`` and
     ``lse`` (unspecified where these are made here)."""
+    if _grad_enabled():
+        _untracked("qknorm_kv4_attention", q)
     T, W, sq, dev, dt = _first(q, "q")
     ptrs, (pages, ps, hk, d) = _kv4_args(cache, dev)
     hq = _heads(W, d, "q")

@@ -254,3 +254,59 @@ def test_attention_bounds_at_the_ends_of_their_type(lib, kw, status):
     # one sequence: its page table of 2^31 entries stays below the next address
     st = lib.qknorm_kv4_attention(*rc.attn_args(**{"T": 1, "B": 1, "bt": 1 << 44, **kw}))
     assert st == status, lib.qknorm_last_error()
+
+
+# --------------------------------------------------------------------------- autograd
+
+def test_operands_that_autograd_follows_are_refused():
+    """Every call that would drop a gradient says so (the operands' devices are looked at later)."""
+    x, one, cs = torch.zeros((2, 128)), torch.ones(64), rc.table(4, 64)
+    pos, cache = torch.zeros(2, dtype=torch.int64), qk.kv4_cache(2, 16, 2, 64, "cpu")
+    bt, lens, pages = torch.zeros((2, 1), dtype=torch.int32), torch.ones(2, dtype=torch.int32), torch.zeros((2, 16, 2, 64))
+    calls = [(lambda q, k, v, gq, gk: qk.qknorm_headwise_rope(q, k, gq, gk, 64, cs, pos), (0, 1, 3, 4)),
+             (lambda q, k, v, gq, gk: qk.qknorm_headwise_rope_backward(q, k, x, x, gq, gk, 64, cs, pos), (0, 1)),
+             (lambda q, k, v, gq, gk: qk.qknorm_rope_append(q, k, v, gq, gk, 64, cs, pos, pages, pages.clone(), pos), range(5)),
+             (lambda q, k, v, gq, gk: qk.qknorm_rope_append_kv4(q, k, v, gq, gk, cs, pos, cache, pos), range(5)),
+             (lambda q, k, v, gq, gk: qk.qknorm_kv4_attention(q, cache, bt, lens, max_seq_len=16), (0,))]
+    for call, tracked in calls:
+        for i in tracked:
+            args = [x.clone(), x.clone(), x.clone(), one.clone(), one.clone()]
+            args[i].requires_grad_()
+            with pytest.raises(ValueError, match="autograd"):
+                call(*args)
+            with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+                call(*args)
+
+
+@pytest.mark.gpu
+def test_a_training_step_in_an_autograd_function():
+    """Forward and gradient in a torch.autograd.Function as a user writes it,
+    against autograd through the formula in 64 bits; grads that come as an
+    expanded scalar are made rows first, gammas get their own type back."""
+    g = torch.Generator().manual_seed(18)
+    T, hq, hk, D = 21, 4, 2, 64
+    cs, pos = rc.table(40, D), torch.randint(0, 40, (T,), generator=g)
+
+    class Rope(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, gq, gk):
+            ctx.save_for_backward(q, k, gq, gk)
+            return qk.qknorm_headwise_rope(q, k, gq, gk, D, cs.to(DEV), pos.to(DEV))
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dq, dk):
+            q, k, gq, gk = ctx.saved_tensors
+            dq, dk, dgq, dgk = qk.qknorm_headwise_rope_backward(dq.contiguous(), dk.contiguous(), q, k, gq, gk, D, cs.to(DEV),
+                                                                pos.to(DEV))
+            return dq, dk, dgq.to(gq.dtype), dgk.to(gk.dtype)
+    leaves = [torch.randn((T, h * D), generator=g).to(DEV).requires_grad_() for h in (hq, hk)]
+    leaves += [rc.gamma_of(D, F32, g).to(DEV).requires_grad_() for _ in range(2)]
+    w = torch.randn((T, hq * D), generator=g).to(DEV)
+    q, k = Rope.apply(*leaves)
+    ((q * w).sum() + k.sum()).backward()
+    for x, dy, gm, dx, dg in ((leaves[0], w, leaves[2], leaves[0].grad, leaves[2].grad),
+                              (leaves[1], torch.ones_like(leaves[1]), leaves[3], leaves[1].grad, leaves[3].grad)):
+        want, mag, want_g, mag_g = rc.gradient(x, dy, gm, D, cs, pos, False)
+        rc.check(dx, want, mag, F32, rel=2.0 ** -16)
+        assert bool(((rc.f64(dg) - want_g).abs() <= (2.0 ** -17 + T * hq * 2.0 ** -24) * mag_g + 1e-30).all())
