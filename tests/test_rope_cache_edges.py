@@ -13,7 +13,7 @@ import attention_normalization_b200 as qk
 import test_rope_cache as rc
 from attention_normalization_b200 import _clib, rope_cache
 from attention_normalization_b200 import build as qbuild
-from test_rope_cache import BF16, DEV, EPS, F32
+from test_rope_cache import BF16, DEV, EPS, F16, F32
 
 
 # --------------------------------------------------------------------------- 4-bit append
@@ -310,3 +310,151 @@ def test_a_training_step_in_an_autograd_function():
         want, mag, want_g, mag_g = rc.gradient(x, dy, gm, D, cs, pos, False)
         rc.check(dx, want, mag, F32, rel=2.0 ** -16)
         assert bool(((rc.f64(dg) - want_g).abs() <= (2.0 ** -17 + T * hq * 2.0 ** -24) * mag_g + 1e-30).all())
+
+
+# --------------------------------------------------------------------------- sizes at which the kernels' loops go round
+#
+# The vector kernels take several lots of a token's heads in one warp from 24
+# warps' rows per SM on (14208 rows of 128 dims of bf16, twice that of 64 dims),
+# the gradient's CTAs take tokens in turn from 2368 warps' on.  Head counts leave
+# a remainder in the last lot.
+
+LARGE = [  # T, q heads, k heads, D, rotary, interleaved, pad, shift
+    (3001, 13, 5, 128, 128, False, 0, 0),
+    (3001, 13, 5, 128, 64, True, 16, 0),
+    (2503, 19, 3, 64, 64, False, 0, 0),
+    (3001, 11, 3, 96, 96, True, 0, 0),
+    (2003, 7, 3, 256, 128, False, 0, 0),
+    (1501, 13, 5, 128, 128, False, 0, 1),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32, rc.E4M3])
+@pytest.mark.parametrize("T,hq,hk,D,rot,inter,pad,shift", LARGE)
+def test_rotation_of_many_rows(T, hq, hk, D, rot, inter, pad, shift, dtype):
+    g = torch.Generator().manual_seed(T + D)
+    _, q = rc.rows_of(T, hq * D, dtype, g, pad, shift)
+    _, k = rc.rows_of(T, hk * D, dtype, g, pad, shift)
+    gq, gk = rc.gamma_of(D, dtype, g), rc.gamma_of(D, dtype, g)
+    P = 997
+    cs, pos = rc.table(P, rot), torch.randint(-40, P + 40, (T,), generator=g)
+    args = (gq.to(DEV), gk.to(DEV), D, cs.to(DEV), pos.to(DEV), EPS)
+    qo, ko = qk.qknorm_headwise_rope(q, k, *args, interleaved=inter)
+    for got, x, gm in ((qo, q, gq), (ko, k, gk)):
+        rc.check(got, *rc.forward(x, gm, D, cs, pos, inter), dtype)
+    for a, b in zip(qk.qknorm_headwise_rope(q, k, *args, interleaved=inter, q_out=q, k_out=k), (qo, ko)):
+        assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("T,hq,hk,D,rot,inter,pad,shift", [*LARGE, (9000, 40, 8, 128, 128, False, 0, 0), (20011, 5, 2, 64, 32, True, 0, 0)])
+def test_gradient_of_many_rows(T, hq, hk, D, rot, inter, pad, shift, dtype):
+    g = torch.Generator().manual_seed(T + D)
+    (_, q), (_, k), (_, dq), (_, dk) = (rc.rows_of(T, h * D, dtype, g, p, shift) for h, p in ((hq, pad), (hk, 0), (hq, 2 * pad), (hk, pad)))
+    gq, gk = rc.gamma_of(D, dtype, g), rc.gamma_of(D, dtype, g)
+    P = 997
+    cs, pos = rc.table(P, rot), torch.randint(-40, P, (T,), generator=g)
+    args = (gq.to(DEV), gk.to(DEV), D, cs.to(DEV), pos.to(DEV), EPS)
+    out = qk.qknorm_headwise_rope_backward(dq, dk, q, k, *args, interleaved=inter)
+    for got, dg, x, dy, gm in ((out[0], out[2], q, dq, gq), (out[1], out[3], k, dk, gk)):
+        dx, dx_mag, want, mag = rc.gradient(x, dy, gm, D, cs, pos, inter)
+        rc.check(got, dx, dx_mag, dtype, rel=2.0 ** -16)
+        # dgamma: 2368 warps; a lane adds T * heads / 2368 products at most and one lot more of each item it takes
+        # (under 200 here), then 5 + 8 + 19 + 32 sums in fixed order
+        assert T * max(hq, hk) / 2368 < 160
+        assert bool(((rc.f64(dg) - want).abs() <= (2.0 ** -17 + 264 * 2.0 ** -24) * mag + 1e-30).all())
+    again = qk.qknorm_headwise_rope_backward(dq, dk, q, k, *args, interleaved=inter)
+    inside = qk.qknorm_headwise_rope_backward(dq, dk, q.clone(), k.clone(), *args, interleaved=inter, dq_in=dq, dk_in=dk)
+    for a, b, c in zip(out, again, inside):
+        assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("layout", ["tokens first", "heads first"])
+@pytest.mark.parametrize("T,hq,hk,D,rot,inter,norm", [
+    (3001, 13, 5, 128, 128, False, True), (2503, 19, 11, 64, 64, True, False), (3001, 0, 7, 128, 64, False, True)])
+def test_append_of_many_rows(T, hq, hk, D, rot, inter, norm, layout, dtype):
+    g = torch.Generator().manual_seed(T + D)
+    ps = 32
+    W = (hq + 2 * hk) * D
+    _, x = rc.rows_of(T, W, dtype, g)
+    q, k, v = x[:, :hq * D] if hq else None, x[:, hq * D:(hq + hk) * D], x[:, (hq + hk) * D:]
+    gq, gk = (rc.gamma_of(D, dtype, g), rc.gamma_of(D, dtype, g)) if norm else (None, None)
+    P = 997
+    cs, pos = rc.table(P, rot), torch.randint(-40, P + 40, (T,), generator=g)
+    pages = T // ps + 4
+    slots = rc.slots_of(T, pages, ps, g)
+    buf, kc, vc = rc.caches_of(layout, pages, ps, hk, D, dtype, g)
+    bits = {2: torch.int16, 4: torch.int32}[buf.element_size()]
+    want_v = vc.cpu()
+    kept = kc.cpu()
+    to = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+    qo = qk.qknorm_rope_append(q, k, v, to(gq), to(gk), D, to(cs), to(pos), kc, vc, to(slots), EPS, interleaved=inter)
+    if hq:
+        rc.check(qo, *rc.forward(q, gq, D, cs, pos, inter), dtype)
+    held = (slots >= 0) & (slots < pages * ps)
+    at = (slots[held] // ps, slots[held] % ps)
+    y, mag = rc.forward(k, gk, D, cs, pos, inter)
+    rc.check(kc.cpu()[at], y[held], mag[held], dtype)
+    want_v[at] = v.cpu().reshape(T, hk, D)[held]
+    assert torch.equal(vc.cpu().contiguous().view(bits), want_v.contiguous().view(bits))
+    other = torch.ones((pages, ps), dtype=torch.bool)
+    other[at] = False
+    assert torch.equal(kc.cpu()[other].view(bits), kept[other].view(bits))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,hq,hk,D,rot,inter,norm", [
+    (3001, 13, 5, 128, 128, False, True), (1501, 2, 21, 128, 64, True, True), (3001, 0, 19, 64, 64, False, True),
+    (2003, 3, 9, 256, 256, False, False)])
+def test_append_kv4_of_many_rows(T, hq, hk, D, rot, inter, norm, dtype):
+    """Codes and scales to the last one, at sizes where some keys lie next to a border."""
+    g = torch.Generator().manual_seed(T + D)
+    ps = 32
+    W = (hq + 2 * hk) * D
+    _, x = rc.rows_of(T, W, dtype, g)
+    q, k, v = x[:, :hq * D] if hq else None, x[:, hq * D:(hq + hk) * D], x[:, (hq + hk) * D:]
+    gq, gk = (rc.gamma_of(D, dtype, g), rc.gamma_of(D, dtype, g)) if norm else (None, None)
+    P = 997
+    cs, pos = rc.table(P, rot), torch.randint(-40, P + 40, (T,), generator=g)
+    pages = T // ps + 4
+    slots = rc.slots_of(T, pages, ps, g)
+    cache = qk.kv4_cache(pages, ps, hk, D, DEV)
+    to = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+    qo = qk.qknorm_rope_append_kv4(q, k, v, to(gq), to(gk), to(cs), to(pos), cache, to(slots), EPS, interleaved=inter)
+    if hq:
+        rc.check(qo, *rc.forward(q, gq, D, cs, pos, inter), dtype)
+    held = (slots >= 0) & (slots < pages * ps)
+    page, off = slots[held] // ps, slots[held] % ps
+    for y, codes, scales in ((rc.forward(k, gk, D, cs, pos, inter)[0], *cache[:2]), (rc.f64(v).reshape(T, hk, D), *cache[2:])):
+        c, s = rc.quantise(y[held].numpy())
+        want_c, want_s = torch.full(codes.shape[:-1] + (D,), 8, dtype=torch.uint8), torch.zeros(scales.shape, dtype=torch.float16)
+        want_c[page, :, off], want_s[page, :, off] = torch.from_numpy(c), torch.from_numpy(s)
+        assert torch.equal(rc.unpack(codes.cpu()), want_c)
+        assert torch.equal(scales.cpu().view(torch.int16)[~want_s.isnan()], want_s.view(torch.int16)[~want_s.isnan()])
+        assert torch.equal(scales.cpu().isnan(), want_s.isnan())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,dtype", [(128, BF16), (64, F16), (256, BF16)])
+@pytest.mark.parametrize("hq,hk,qn,lens,window,sharp", [
+    (8, 2, [4, 4], [5000, 4999], 0, 1.0), (8, 2, [5, 0, 2], [3000, 2500, 1700], 0, 8.0), (6, 2, [9, 6], [4100, 1100], 900, 1.0),
+    (2, 1, [11], [9001], 0, 8.0), (20, 1, [1, 2], [2100, 4000], 0, 1.0)])
+def test_attention_of_chunks_over_long_caches(hq, hk, qn, lens, window, sharp, D, dtype):
+    """Several query tiles a sequence, cut into shares; with sharp scores the
+    references move on the way."""
+    g = torch.Generator().manual_seed(sum(lens) + D)
+    ps = 32
+    pages = sum(-(-n // ps) for n in lens) + 1
+    cache = rc.random_cache(pages, ps, hk, D, g)
+    q_start = torch.tensor([0] + qn).cumsum(0).int()
+    q = torch.randn((int(q_start[-1]) + 1, hq * D), generator=g).to(dtype).to(DEV)
+    args = (q, cache, rc.tables(lens, ps, pages, g), torch.tensor(lens, dtype=torch.int32), q_start, max(qn), max(lens), window)
+    assert qk.kv4_attention_workspace_bytes(q.shape[0], len(qn), hq, hk, D, max(qn), max(lens)) > 0
+    got, lse = rc.check_attention(*args, scale=sharp / math.sqrt(D))
+    again, lse2 = rc.run_attention(*args, scale=sharp / math.sqrt(D))
+    assert torch.equal(got, again) and torch.equal(lse, lse2)
