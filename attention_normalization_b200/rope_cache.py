@@ -83,6 +83,13 @@ def _flat(t, name, n, dtype, index):
     return t.data_ptr()
 
 
+def _int32(**sizes):
+    """Refuses sizes that the library's 32-bit arguments cannot hold: ctypes would cut them off."""
+    for name, n in sizes.items():
+        if not -1 << 31 <= n < 1 << 31:
+            raise ValueError(f"{name} = {n} must be below 2**31")
+
+
 def _table(cos_sin, index):
     if not isinstance(cos_sin, _Tensor) or cos_sin.dtype is not torch.float32 or cos_sin.get_device() != index \
             or len(cos_sin.shape) != 2 or not cos_sin.is_contiguous():
@@ -143,6 +150,7 @@ def qknorm_headwise_rope(q_in: torch.Tensor, k_in: torch.Tensor, gamma_q: torch.
 
 def rope_backward_workspace_bytes(T: int, q_heads: int, k_heads: int, head_dim: int) -> int:
     """Workspace ``qknorm_headwise_rope_backward`` needs."""
+    _int32(q_heads=q_heads, k_heads=k_heads, head_dim=head_dim)
     n = capi().qknorm_headwise_rope_backward_workspace_bytes(T, q_heads, k_heads, head_dim)
     if n < 0:
         raise ValueError("invalid sizes for the gradient's workspace")
@@ -366,6 +374,7 @@ def kv4_attention_workspace_bytes(T: int, batch: int, q_heads: int, kv_heads: in
                                   max_seq_len: int) -> int:
     """Workspace that serves every ``qknorm_kv4_attention`` with these heads and
     at most this batch, ``max_q_len`` and ``max_seq_len``."""
+    _int32(batch=batch, q_heads=q_heads, kv_heads=kv_heads, head_dim=head_dim, max_q_len=max_q_len, max_seq_len=max_seq_len)
     n = capi().qknorm_kv4_attention_workspace_bytes(T, batch, q_heads, kv_heads, head_dim, max_q_len, max_seq_len)
     if n < 0:
         raise ValueError("invalid sizes for the attention's workspace")
@@ -386,6 +395,8 @@ def qknorm_kv4_attention(q: torch.Tensor, cache, block_table: torch.Tensor, seq_
     ``lse`` (unspecified where these are made here)."""
     if _grad_enabled():
         _untracked("qknorm_kv4_attention", q)
+    if (max_seq_len | max_q_len | window) >> 31:
+        _int32(max_seq_len=max_seq_len, max_q_len=max_q_len, window=window)
     T, W, sq, dev, dt = _first(q, "q")
     ptrs, (pages, ps, hk, d) = _kv4_args(cache, dev)
     hq = _heads(W, d, "q")

@@ -458,3 +458,25 @@ def test_attention_of_chunks_over_long_caches(hq, hk, qn, lens, window, sharp, D
     got, lse = rc.check_attention(*args, scale=sharp / math.sqrt(D))
     again, lse2 = rc.run_attention(*args, scale=sharp / math.sqrt(D))
     assert torch.equal(got, again) and torch.equal(lse, lse2)
+
+
+# --------------------------------------------------------------------------- sizes past 32 bits
+
+@pytest.mark.parametrize("size", [2 ** 31, 2 ** 32, 2 ** 32 + 16, 2 ** 40, -2 ** 32 + 16])
+def test_bounds_past_32_bits_are_refused_not_cut_off(size):
+    """2^32 as "no bound" would otherwise arrive as 0 and cut every sequence there."""
+    x, cache = torch.zeros((1, 128), dtype=BF16), qk.kv4_cache(1, 16, 1, 128, "cpu")
+    bt, lens = torch.zeros((1, 1), dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    for kw in ({"max_seq_len": size}, {"max_seq_len": 16, "max_q_len": size}, {"max_seq_len": 16, "window": size}):
+        with pytest.raises(ValueError, match="2\\*\\*31"):
+            qk.qknorm_kv4_attention(x, cache, bt, lens, **kw)
+    for i in range(1, 7):
+        args = [1, 1, 8, 8, 128, 1, 16]
+        args[i] = size
+        with pytest.raises(ValueError, match="2\\*\\*31"):
+            qk.kv4_attention_workspace_bytes(*args)
+    for i in range(1, 4):
+        args = [1, 8, 8, 128]
+        args[i] = size
+        with pytest.raises(ValueError, match="2\\*\\*31"):
+            qk.rope_backward_workspace_bytes(*args)
