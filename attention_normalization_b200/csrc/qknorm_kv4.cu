@@ -865,17 +865,21 @@ int64_t share_ctas(int64_t units, int64_t tiles, int64_t slots) {
 // Shorter sequences are never cut into shares.
 constexpr int64_t kWholeTiles = 64;
 
-Plan plan(int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t max_q_len, int32_t max_seq_len) {
+Plan plan(int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t max_q_len, int32_t max_seq_len,
+          int32_t window) {
     int64_t slots = 0;
     Plan pl = tiled(B, q_heads, kv_heads, head_dim, max_q_len, &slots);
     const int64_t units = pl.pairs * kv_heads, tiles = ((int64_t)max_seq_len + 15) / 16;
+    // what a unit reads at most: with a window no more than its rows see (64 sequences to 32768 tokens, a window of 512,
+    // whole units 21 us, shares 28; 4 with a window of 2048 18.6 and 15.8)
+    const int64_t seen = window > 0 ? ((int64_t)window + max_q_len - 1 + 15) / 16 : tiles, longest = seen < tiles ? seen : tiles;
     // One CTA a unit where units are many, or short enough that shares and a join
     // cost more than their balance gains (whole units against shares, one token a
     // sequence, 32 heads over 8 of 128: 128 sequences to 4096 tokens 104 against
     // 107 us, 128 to 2048 60 against 69, 64 to 4096 65 against 60.5, 64 to 2048
     // 38.5 against 40.9, 64 to 1024 24.7 against 30.5, 16 to 8192 59 against 36,
     // 4 to 2048 17.7 against 12.4, 4 to 1024 10.5 against 12.5).
-    if (units >= 2 * slots || tiles <= kWholeTiles || (units >= slots && tiles <= 128) ||
+    if (units >= 2 * slots || longest <= kWholeTiles || (units >= slots && longest <= 128) ||
         units * (tiles + kUnitCost) >= ((int64_t)1 << 31))
         return pl;
     pl.ctas = (int32_t)share_ctas(units, tiles, slots);
@@ -978,7 +982,7 @@ qkn_status qknorm_kv4_attention(const void *q, int64_t q_stride, void *out, int6
     const int64_t held = (int64_t)max_pages * page_size, longest = held < max_seq_len ? held : max_seq_len;
     if (longest > kMaxTokens)
         return fail(QKN_ERR_UNSUPPORTED, "sequences of up to %lld tokens, at most %lld", (long long)longest, (long long)kMaxTokens);
-    const Plan pl = plan(B, q_heads, kv_heads, head_dim, max_q_len, max_seq_len);
+    const Plan pl = plan(B, q_heads, kv_heads, head_dim, max_q_len, max_seq_len, window);
     const int64_t need = share_bytes(pl.ctas, pl.pairs, pl.n_tiles, head_dim);
     if (workspace_bytes < need || (need > 0 && !workspace))
         return fail(QKN_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)need);

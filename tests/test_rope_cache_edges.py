@@ -480,3 +480,35 @@ def test_bounds_past_32_bits_are_refused_not_cut_off(size):
         args[i] = size
         with pytest.raises(ValueError, match="2\\*\\*31"):
             qk.rope_backward_workspace_bytes(*args)
+
+
+# --------------------------------------------------------------------------- whole units or shares
+
+def needs_workspace(lib, **kw):
+    """Whether the call cuts its units into shares: it then refuses an absent workspace."""
+    st = lib.qknorm_kv4_attention(*rc.attn_args(**{"qs": 1 << 13, "os": 1 << 13, "lse": 0, "qst": rc.at(10), "ws": 0, "wb": 0,
+                                                   "mp": 1 << 17, **kw}))
+    assert st in (rc.CUDA, rc.INVALID), lib.qknorm_last_error()
+    return st == rc.INVALID
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="an accepted call with made-up addresses is not launched")
+def test_units_are_as_long_as_their_window(lib):
+    long = dict(T=64, B=64, mq=1, ml=32768)
+    assert needs_workspace(lib, **long)
+    assert not needs_workspace(lib, **long, win=512)
+    assert needs_workspace(lib, **{**long, "B": 4, "T": 4}, win=2048)
+    assert not needs_workspace(lib, **{**long, "B": 4, "T": 4}, win=1024)
+    assert not needs_workspace(lib, **{**long, "B": 4, "T": 4, "ml": 1024}, win=4096)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,hq,hk,rows,window", [(128, 8, 2, 1, 500), (64, 8, 8, 1, 17), (256, 4, 1, 3, 300), (128, 16, 2, 5, 1000)])
+def test_attention_in_a_window_of_a_long_cache(D, hq, hk, rows, window):
+    g = torch.Generator().manual_seed(D + window)
+    ps, lens, qn = 32, [6000, 40, 2777], [rows, rows, 1]
+    pages = sum(-(-n // ps) for n in lens) + 1
+    cache = rc.random_cache(pages, ps, hk, D, g)
+    q_start = torch.tensor([0] + qn).cumsum(0).int()
+    q = torch.randn((int(q_start[-1]), hq * D), generator=g).to(BF16).to(DEV)
+    rc.check_attention(q, cache, rc.tables(lens, ps, pages, g), torch.tensor(lens, dtype=torch.int32), q_start, rows, 6000, window)
