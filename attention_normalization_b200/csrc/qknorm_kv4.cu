@@ -862,8 +862,8 @@ int64_t share_ctas(int64_t units, int64_t tiles, int64_t slots) {
     return most < slots ? most : slots;
 }
 
-// Shorter sequences are never cut into shares.
-constexpr int64_t kWholeTiles = 64;
+// Units of at most so many tiles are never cut into shares (see plan()).
+int64_t whole_tiles(int32_t head_dim) { return head_dim == 64 ? 128 : 64; }
 
 Plan plan(int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t max_q_len, int32_t max_seq_len,
           int32_t window) {
@@ -874,14 +874,22 @@ Plan plan(int32_t B, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_
     // whole units 21 us, shares 28; 4 with a window of 2048 18.6 and 15.8)
     const int64_t seen = window > 0 ? ((int64_t)window + max_q_len - 1 + 15) / 16 : tiles, longest = seen < tiles ? seen : tiles;
     // One CTA a unit where units are many, or short enough that shares and a join
-    // cost more than their balance gains (whole units against shares, one token a
-    // sequence, 32 heads over 8 of 128: 128 sequences to 4096 tokens 104 against
-    // 107 us, 128 to 2048 60 against 69, 64 to 4096 65 against 60.5, 64 to 2048
-    // 38.5 against 40.9, 64 to 1024 24.7 against 30.5, 16 to 8192 59 against 36,
-    // 4 to 2048 17.7 against 12.4, 4 to 1024 10.5 against 12.5).
-    if (units >= 2 * slots || longest <= kWholeTiles || (units >= slots && longest <= 128) ||
-        units * (tiles + kUnitCost) >= ((int64_t)1 << 31))
-        return pl;
+    // cost more than their balance gains.  Whole units against shares in us, 32
+    // heads over 8, B sequences to L tokens:
+    //   one token each, 128 dims: 128 to 4096 104 / 107, 128 to 2048 60 / 69, 64 to 4096 65 / 60.5,
+    //     64 to 2048 38.5 / 40.9, 64 to 1024 24.7 / 30.5, 16 to 8192 59 / 36, 8 to 2048 17.6 / 15.3,
+    //     4 to 2048 17.7 / 12.4, 4 to 1024 10.5 / 12.5;
+    //   64 dims, where a tile is half the work: 128 to 4096 67 / 73, 64 to 4096 48 / 43, 64 to 2048 26.5 / 30.7,
+    //     16 to 4096 22.8 / 19.4, 16 to 2048 13.1 / 18.1, 8 to 2048 12.8 / 12.9, 4 to 4096 22.4 / 13.0, 4 to 2048 12.8 / 12.0;
+    //   256 dims: 128 to 2048 119 / 127, 64 to 2048 73 / 72, 64 to 1024 44 / 50, 16 to 2048 31.6 / 28.2, 16 to 1024 18.9 / 22.9,
+    //     4 to 2048 30.4 / 17.7, 4 to 1024 18.3 / 17.4, 4 to 512 11.5 / 17.4;
+    //   tiles of 16 rows, whose shares cost more to join, 128 dims (444 CTAs at once): 4 chunks of 64 (512 units) to 4096
+    //     75 / 104, to 16384 274 / 282, one of 200 (400 units) to 4096 80 / 105, to 32768 573 / 575, 16 of 9 (384) to 4096
+    //     75 / 79, to 8192 140 / 124, 16 of 8 (256) to 4096 70 / 60; 64 dims (592): 64 of 4 (512) to 4096 58 / 70, to 8192
+    //     108 / 101, 16 of 9 (384) to 4096 55 / 53, 16 of 8 (256) to 2048 22 / 33.
+    const int64_t whole = whole_tiles(head_dim);
+    const bool many = pl.n_tiles == 2 ? 4 * units >= 3 * slots && longest <= 256 : units >= slots && longest <= 2 * whole;
+    if (units >= 2 * slots || longest <= whole || many || units * (tiles + kUnitCost) >= ((int64_t)1 << 31)) return pl;
     pl.ctas = (int32_t)share_ctas(units, tiles, slots);
     return pl;
 }
@@ -940,7 +948,7 @@ int64_t qknorm_kv4_attention_workspace_bytes(int64_t T, int32_t B, int32_t q_hea
     int64_t slots = 0;
     const Plan pl = tiled(B, q_heads, kv_heads, head_dim, max_q_len, &slots);
     const int64_t tiles = ((int64_t)max_seq_len + 15) / 16;
-    if (tiles <= kWholeTiles) return 0;
+    if (tiles <= whole_tiles(head_dim)) return 0;
     const int64_t units = pl.pairs * kv_heads < 2 * slots ? pl.pairs * kv_heads : 2 * slots - 1;
     return share_bytes(share_ctas(units, tiles, slots), units / kv_heads, pl.n_tiles, head_dim);
 }

@@ -512,3 +512,15 @@ def test_attention_in_a_window_of_a_long_cache(D, hq, hk, rows, window):
     q_start = torch.tensor([0] + qn).cumsum(0).int()
     q = torch.randn((int(q_start[-1]), hq * D), generator=g).to(BF16).to(DEV)
     rc.check_attention(q, cache, rc.tables(lens, ps, pages, g), torch.tensor(lens, dtype=torch.int32), q_start, rows, 6000, window)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="an accepted call with made-up addresses is not launched")
+@pytest.mark.parametrize("D,B,rows,L,shares", [
+    (128, 64, 1, 4096, True), (128, 64, 1, 2048, False), (128, 4, 1, 2048, True), (128, 4, 1, 1024, False), (128, 128, 1, 4096, False),
+    (64, 64, 1, 4096, True), (64, 16, 1, 4096, True), (64, 16, 1, 2048, False), (64, 128, 1, 4096, False),
+    (256, 16, 1, 2048, True), (256, 64, 1, 1024, False), (256, 4, 1, 1024, False),
+    (128, 64, 4, 4096, False), (128, 16, 8, 4096, True), (64, 64, 4, 4096, False), (64, 16, 8, 2048, False),
+    (128, 1, 200, 4096, False), (128, 16, 9, 8192, True), (64, 64, 4, 8192, True)])
+def test_units_are_cut_where_that_was_faster(lib, D, B, rows, L, shares):
+    """The rule's two sides at sizes where both were measured (the comment beside it)."""
+    assert needs_workspace(lib, D=D, B=B, T=B * rows, mq=rows, ml=L) == shares
