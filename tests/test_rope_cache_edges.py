@@ -524,3 +524,33 @@ def test_attention_in_a_window_of_a_long_cache(D, hq, hk, rows, window):
 def test_units_are_cut_where_that_was_faster(lib, D, B, rows, L, shares):
     """The rule's two sides at sizes where both were measured (the comment beside it)."""
     assert needs_workspace(lib, D=D, B=B, T=B * rows, mq=rows, ml=L) == shares
+
+
+# --------------------------------------------------------------------------- in place on packed rows
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("T,hq,hk,D,rot,inter", [(1, 4, 2, 128, 128, False), (50, 6, 2, 64, 32, True), (3001, 13, 5, 128, 128, False)])
+def test_append_with_its_q_rows_in_place(T, hq, hk, D, rot, inter, shift):
+    """Q's columns of packed rows turned where they are, K's and V's beside them read."""
+    g = torch.Generator().manual_seed(T + D)
+    ps, W = 16, (hq + 2 * hk) * D
+    pages = T // ps + 4
+    buf, _ = rc.rows_of(T, W, BF16, g, 16, shift)
+    gm, cs = rc.gamma_of(D, BF16, g).to(DEV), rc.table(64, rot).to(DEV)
+    pos, slots = torch.randint(-2, 66, (T,), generator=g).to(DEV), rc.slots_of(T, pages, ps, g).to(DEV)
+    caches = [[torch.zeros((pages, ps, hk, D), dtype=BF16, device=DEV) for _ in range(2)] for _ in range(2)]
+    four = [qk.kv4_cache(pages, ps, hk, D, DEV) for _ in range(2)]
+
+    def rows():  # at the same alignment each time: the element-wise kernel sums in another order
+        r = buf.clone()[shift:shift + T * (W + 16)].view(T, W + 16)
+        return r[:, :hq * D], r[:, hq * D:(hq + hk) * D], r[:, (hq + hk) * D:W]
+    now, now4, kept = rows(), rows(), rows()
+    apart = qk.qknorm_rope_append(*kept, gm, gm, D, cs, pos, *caches[0], slots, interleaved=inter)
+    inside = qk.qknorm_rope_append(*now, gm, gm, D, cs, pos, *caches[1], slots, interleaved=inter, q_out=now[0])
+    apart4 = qk.qknorm_rope_append_kv4(*kept, gm, gm, cs, pos, four[0], slots, interleaved=inter)
+    inside4 = qk.qknorm_rope_append_kv4(*now4, gm, gm, cs, pos, four[1], slots, interleaved=inter, q_out=now4[0])
+    assert inside is now[0] and inside4 is now4[0]
+    for a, b in ((apart, inside), (apart4, inside4), *zip(caches[0], caches[1]), *zip(four[0], four[1]), *zip(now[1:], kept[1:]),
+                 *zip(now4[1:], kept[1:])):
+        assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
