@@ -102,10 +102,10 @@ inline qkn_status check_kv4(int64_t num_pages, int32_t page_size, int32_t kv_hea
 // One launch with programmatic stream serialization (the kernel waits for the
 // one before it itself).
 template <typename P>
-inline cudaError_t launch_pdl(const void *fn, dim3 grid, unsigned block, size_t smem, void *stream, const P &p) {
+inline cudaError_t launch_pdl(const void *fn, dim3 grid, dim3 block, size_t smem, void *stream, const P &p) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(block);
+    cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];

@@ -127,10 +127,11 @@ __device__ __forceinline__ float finish_lse(float m, float total) {  // base 2 -
 // only when a scaled weight would exceed 2^15, or a weight 2^75 where the values
 // are (nearly) zeros: one vote per step.  The exact maximum is not needed, as O
 // has its group's reference until the end and l the first group's.
-// Instructions bound it: 300 a warp for 16 tokens of 128 dims and 8 rows, 146 of
-// them codes to halves and 16 products (one B200: one token for each of 64
-// sequences of 1024 to 4096 tokens, 32 heads over 8, 60 us, 3.0 TB/s; one of
-// 131072 tokens 45 us, 3.2 TB/s; the loads alone take 47 and 41 us).  4 warps a
+// Instructions bound it: about 300 a warp for 16 tokens of 128 dims and 8 rows,
+// 146 of them codes to halves and 16 products (one B200: one token for each of 64
+// sequences of 1024 to 4096 tokens, 32 heads over 8, 61 us, 2.9 TB/s; one of
+// 131072 tokens 45 us, 3.2 TB/s; the loads alone take 47 and 41 us; with one
+// reference for all groups 60 and 45 us).  4 warps a
 // CTA: with 8 the batch took 72 us.
 constexpr int kAttnWarps = 4;
 constexpr int kLeastShare = 32;  // tiles: 8 for each warp
@@ -709,9 +710,10 @@ __device__ __forceinline__ Share find_share(const Kv4AttnParams &p, int tile_row
     return found;
 }
 
-// CTAs resident on an SM.  Of 128 dims three: with 8 rows (158 registers) 131072
-// tokens take 46 us where four (128 registers) take 50, with 16 rows chunks take
-// 340 us where two (no spills) take 386.
+// CTAs resident on an SM.  Of 128 dims three: with 8 rows (160 registers) 131072
+// tokens take 45 us where four (128 registers) take 50, with 16 rows (168, and 104
+// bytes of spills a thread) chunks take 346 us where two without spills took 386.
+// Of 64 dims the spills are 48 bytes.
 template <int D, int NT>
 constexpr int kResident = D == 64 ? (NT == 1 ? 5 : 4) : D == 128 ? 3 : 2;
 

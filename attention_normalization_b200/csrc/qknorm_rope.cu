@@ -12,8 +12,10 @@
 // 4 bits: a group of 64 elements has s = fp16(max |y| / 7) and codes
 //   clamp(rint(y / s), -7, 7).
 //
-// Every kernel is bound by memory traffic: each element is read once and
-// written once (the gradient reads two rows and writes one).
+// The vector kernels read each element once and write it once (the gradient reads
+// two rows and writes one); memory traffic bounds the rotation, its gradient and
+// the element append, instructions the 4-bit append.  The element-wise kernels
+// read a head twice, the second time from cache.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -58,7 +60,7 @@ __device__ __forceinline__ double norm_factor(double s, const RopeParams &p) {
 // depend on the kernel variant that wrote it: 32 bits alone put about one code in
 // a million on the other side of its border.  The vector kernel decides in 32
 // bits where their error allows it and comes here otherwise (4096 tokens, 8 heads
-// of 128: 37 us for the append; 67 us with every key in 64 bits).
+// of 128: 34 us for the append; 67 us with every key in 64 bits).
 __device__ __forceinline__ __half kv4_scale(double amax, bool bad) {
     if (bad) return __ushort_as_half(0x7FFFu);  // a NaN or infinity in the group: the group reads as NaN
     return __double2half(fmin(amax / 7.0, 65504.0));
@@ -537,13 +539,6 @@ __device__ __forceinline__ void store_codes(bool interleaved, uint8_t *codes, co
     }
 }
 
-// Which of the head's two blocks (the lane's lo and hi vectors) element i of
-// the first (second = false) or second elements of its pairs lies in.
-template <typename E>
-__device__ __forceinline__ bool in_hi(bool interleaved, bool second, int i) {
-    return interleaved ? i >= Elem<E>::kPerVec / 2 : second;
-}
-
 __device__ __forceinline__ F2 add2(F2 a, F2 b) {
     F2 d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
@@ -659,6 +654,10 @@ constexpr int kManyHeads = 2;  // four at a time: 20.4 us for the prompt below t
 // so short-lived warps need to overlap (4096 tokens, 32 + 8 heads of 128, bf16,
 // packed: 16.5 us at 72 registers, 5.2 TB/s; 17.5 us at the 76 to 108 that the
 // compiler takes by itself, 17.6 at 64; E4M3 at 128, four-bit append at 80).
+// 72 registers spill 8 to 28 bytes a thread, the 80 of the 4-bit append 152 to 248
+// with 16-bit rows, and that is faster all the same where there is work for six
+// CTAs: 4096 tokens of 8 K and 8 V heads of 128 take 34.3 us, 36.1 with five, 38.5
+// with four and no spills; of 64 tokens 6.1, 6.0 and 5.6.
 template <typename E, int SINK>
 constexpr int kVectorResident = SINK == kSinkKv4 ? 6 : sizeof(typename Elem<E>::Bits) == 1 ? 4 : 7;
 
@@ -844,8 +843,8 @@ __global__ void __launch_bounds__(kVectorWarps * 32, kVectorResident<E, SINK>) h
 // dgamma sums in registers, first over Q's heads, then over K's; they are added
 // over the warp's lane groups, then over the warps in order.  128 registers and
 // so 16 warps an SM: 16384 tokens of 40 + 8 heads of 128, bf16, take 122 us with
-// the sum's launch (5.0 TB/s), 136 us at 168 registers; the element-wise kernel
-// 725 us.
+// the sum's launch (5.0 TB/s; 84 to 100 bytes of spills a thread for 16-bit types),
+// 136 us at 168 registers; the element-wise kernel 725 us.
 constexpr int kGradWarps = 8;
 
 template <typename E, int L>
@@ -1032,7 +1031,8 @@ __global__ void __launch_bounds__(32 * kSumRows) dgamma_sum_kernel(const __grid_
 
 // ----------------------------------------------------------------------------
 // Cached tokens of the 4-bit cache back as rows: one thread per 8 elements, a
-// row of threads along a token's K, then V elements.
+// row of threads along a token's K, then V elements.  Bound by the rows written:
+// 4096 tokens of 8 heads of 128 to bf16 take 8.6 us (2.5 TB/s), 64 tokens 1.8 us.
 struct Kv4ReadParams {
     const uint8_t *codes[2];
     const __half *scales[2];
@@ -1656,17 +1656,8 @@ qkn_status qknorm_headwise_rope_backward(const void *q_in, int64_t q_stride, con
     g.dgamma[1] = dgamma_k;
     g.ctas = (int32_t)ctas;
     g.head_dim = head_dim;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((2 * head_dim + 31) / 32));
-    cfg.blockDim = dim3(32, kSumRows);
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    void *args[] = {&g};
-    return launched(cudaLaunchKernelExC(&cfg, (const void *)dgamma_sum_kernel, args));
+    return launched(launch_pdl((const void *)dgamma_sum_kernel, dim3((unsigned)((2 * head_dim + 31) / 32)), dim3(32, kSumRows),
+                               0, stream, g));
 }
 
 }  // extern "C"

@@ -45,7 +45,6 @@ struct RopeParams {
     const int64_t *slots;        // [T] flat token index, negative: not written
     int64_t num_slots;
     int32_t page_size;
-    int32_t pad;
     char *cache[2];
     int64_t page_stride[2], token_stride[2], head_stride[2];
     __half *scales[2];

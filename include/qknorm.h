@@ -348,6 +348,9 @@ qkn_status qknorm_rope_append(const void *q_in, void *q_out, const void *gamma_q
  * float16 rows).  qknorm_kv4_read gives n cached tokens back as K and V rows
  * [n rows, kv_heads * head_dim], each value rounded once; a slot outside the
  * cache gives zeros.
+ * Errors: as qknorm_rope_append, plus QKN_ERR_INVALID_ARG for a cache tensor
+ * that is not 16-byte aligned and, in the read, for n * kv_heads * head_dim
+ * from 2^34 - 1024 on; QKN_ERR_UNSUPPORTED for E4M3 rows.
  */
 qkn_status qknorm_rope_append_kv4(const void *q_in, void *q_out, const void *gamma_q, int64_t q_stride, int32_t q_heads,
                                   const void *k_in, const void *gamma_k, int64_t k_stride, const void *v_in,
