@@ -127,7 +127,7 @@ __device__ __forceinline__ float finish_lse(float m, float total) {  // base 2 -
 // only when a scaled weight would exceed 2^15, or a weight 2^75 where the values
 // are (nearly) zeros: one vote per step.  The exact maximum is not needed, as O
 // has its group's reference until the end and l the first group's.
-// Instructions bound it: about 300 a warp for 16 tokens of 128 dims and 8 rows,
+// Instructions bound it: 308 a warp for 16 tokens of 128 dims and 8 rows,
 // 146 of them codes to halves and 16 products (one B200: one token for each of 64
 // sequences of 1024 to 4096 tokens, 32 heads over 8, 61 us, 2.9 TB/s; one of
 // 131072 tokens 45 us, 3.2 TB/s; the loads alone take 47 and 41 us; with one
