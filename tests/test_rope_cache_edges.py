@@ -554,3 +554,71 @@ def test_append_with_its_q_rows_in_place(T, hq, hk, D, rot, inter, shift):
     for a, b in ((apart, inside), (apart4, inside4), *zip(caches[0], caches[1]), *zip(four[0], four[1]), *zip(now[1:], kept[1:]),
                  *zip(now4[1:], kept[1:])):
         assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+# --------------------------------------------------------------------------- captured, repeated indices
+
+@pytest.mark.gpu
+def test_two_captured_attentions_on_one_workspace():
+    """Cut into shares, two graphs replayed in turn on one buffer, with other
+    lengths and queries each time, against eager calls."""
+    g = torch.Generator().manual_seed(19)
+    hq, hk, D, ps, L, B = 8, 2, 128, 64, 9000, 3
+    pages = -(-L // ps)
+    cache = rc.random_cache(pages, ps, hk, D, g)
+    bt = torch.stack([torch.randperm(pages, generator=g) for _ in range(B)]).int().to(DEV)
+    held = torch.empty(qk.kv4_attention_workspace_bytes(B, B, hq, hk, D, 1, L), dtype=torch.uint8, device=DEV)
+    assert held.numel() > 0
+    q, lens = [torch.zeros((B, hq * D), dtype=BF16, device=DEV) for _ in range(2)], [torch.ones(B, dtype=torch.int32, device=DEV) for _ in range(2)]
+
+    def call(i, **kw):
+        return qk.qknorm_kv4_attention(q[i], cache, bt, lens[i], max_seq_len=L, return_lse=True, **kw)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(0, workspace=held)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for i in range(2):
+        with torch.cuda.graph(graphs[i]):
+            outs.append(call(i, workspace=held))
+    for _ in range(3):
+        for i in range(2):
+            q[i].copy_(torch.randn((B, hq * D), generator=g))
+            lens[i].copy_(torch.randint(0, L + 1, (B,), generator=g))
+        graphs[0].replay()
+        graphs[1].replay()
+        for i in range(2):
+            for a, b in zip(outs[i], call(i)):
+                assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("L", [100, 3000])
+def test_attention_to_the_same_page_over_and_over(L):
+    g = torch.Generator().manual_seed(L)
+    cache = rc.random_cache(3, 32, 2, 128, g)
+    bt = torch.randint(0, 3, (2, -(-L // 32)), generator=g).int()
+    q = torch.randn((2, 4 * 128), generator=g).to(BF16).to(DEV)
+    rc.check_attention(q, cache, bt, torch.tensor([L, L - 31], dtype=torch.int32), None, 1, L)
+
+
+@pytest.mark.gpu
+def test_tokens_on_the_same_slot_disturb_no_other_cell():
+    g = torch.Generator().manual_seed(20)
+    T, hk, D, ps = 64, 2, 128, 16
+    x = torch.randn((T, 2 * hk * D), generator=g).to(BF16).to(DEV)
+    k, v, gm, cs = x[:, :hk * D], x[:, hk * D:], rc.gamma_of(D, BF16, g).to(DEV), rc.table(T, D).to(DEV)
+    pos, once = torch.arange(T, device=DEV), torch.randperm(T + ps, generator=g)[:T]
+    twice = once.clone()
+    twice[::8] = int(once[0])
+    held = [qk.kv4_cache(T // ps + 1, ps, hk, D, DEV) for _ in range(2)]
+    for cache, slots in zip(held, (once, twice)):
+        qk.qknorm_rope_append_kv4(None, k, v, None, gm, cs, pos, cache, slots.to(DEV))
+    alone = torch.ones(T, dtype=torch.bool)
+    alone[::8] = False
+    at = once[alone]
+    for a, b in zip(*held):
+        assert torch.equal(a.cpu()[at // ps, :, at % ps], b.cpu()[at // ps, :, at % ps])
+    other = torch.tensor([s for s in range(T + ps) if s not in twice.tolist()])
+    assert not held[1][1].cpu()[other // ps, :, other % ps].any()
